@@ -247,6 +247,82 @@ BEAM_API beam_status_t beam_moe_forward_boundary(
     int32_t depth_n, float eps, void* h_out, void* x_next, int32_t* topk_ids_out, float* topk_w_out,
     void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Training operators: the products grouped by expert with both gradients, the gradient of the
+ * boundary above, and the orthogonalised update of weight matrices (for training on recorded routes:
+ * [S] §Reinforcement learning in Miles). ---- */
+
+/* Matrix products grouped by expert, rows sorted by expert (as beam_moe_forward sorts its slots; see
+ * BEAM_WS_EXPERT_OFF), ragged: rows [offsets[e], offsets[e + 1]) belong to expert e.
+ *   beam_moe_grouped_mm     out[r] = x[r] . w[e]^T                     (forward)
+ *   beam_moe_grouped_mm_dx  dx[r]  = dy[r] . w[e]                      (gradient of x)
+ *   beam_moe_grouped_mm_dw  dw[e]  = sum over e's rows of dy[r]^T x[r] (gradient of w)
+ *   x          [R][K] bf16
+ *   w          [E][N][K] bf16 (each row along K, as w_gate_up and w_down)
+ *   dy         [R][N] bf16
+ *   offsets    [E + 1] int32 (device), 0 <= offsets[0] <= ... <= offsets[E] <= R. Read on the device:
+ *              values out of range are clamped and a decreasing pair holds no rows (memory-safe, the
+ *              results then unspecified).
+ *   out        [R][N], dx [R][K], dw [E][N][K]: out_dtype (BEAM_F32, or BEAM_BF16 rounded to
+ *              nearest even once, from the FP32 sum)
+ *   Rows before offsets[0] or from offsets[E] on are not read, and their out or dx is left as it was.
+ *   The dw of an expert without rows is zero. R = 0: the first two are no-ops; dw is set to zero (dy
+ *   and x may then both be NULL).
+ * The products are exact and summed in FP32 on the matrix cores, in an order that depends on the
+ * sizes alone: equal calls give equal bits.
+ * Limits: N % 8 == 0, K % 8 == 0, N and K <= 2^20, N * K < 2^31, E <= 4096, R < 2^31. No workspace. */
+BEAM_API beam_status_t beam_moe_grouped_mm(const void* x, const void* w, const int32_t* offsets,
+                                           void* out, int64_t R, int32_t E, int32_t N, int32_t K,
+                                           int32_t out_dtype, void* stream);
+BEAM_API beam_status_t beam_moe_grouped_mm_dx(const void* dy, const void* w, const int32_t* offsets,
+                                              void* dx, int64_t R, int32_t E, int32_t N, int32_t K,
+                                              int32_t out_dtype, void* stream);
+BEAM_API beam_status_t beam_moe_grouped_mm_dw(const void* dy, const void* x, const int32_t* offsets,
+                                              void* dw, int64_t R, int32_t E, int32_t N, int32_t K,
+                                              int32_t out_dtype, void* stream);
+
+/* Gradient of beam_residual_boundary, its roundings passed through as the identity, in FP32:
+ *   g   = d_x_next * gamma_next,  r2 = 1 / sqrt(mean(h'^2) + eps)
+ *   d   = d_h_out + r2 * (g - h' * r2^2 * mean(g * h'));  d_gamma_next = sum_t d_x_next * h' * r2
+ *   d_h = sqrt((n-1)/n) * d,  dp = d / sqrt(n)
+ *   q   = dp * gamma_post,    r1 = 1 / sqrt(mean(u^2) + eps),  u = bf16(y)
+ *   d_y = r1 * (q - u * r1^2 * mean(q * u));              d_gamma_post = sum_t dp * u * r1
+ *   y          [T][hidden] y_dtype: the forward's y
+ *   h_out      [T][hidden] bf16: the forward's h_out (h itself is not needed)
+ *   d_h_out    [T][hidden] bf16: gradient of h_out; NULL: zero
+ *   d_x_next   [T][hidden] bf16: gradient of x_next
+ *   d_y        [T][hidden] y_dtype out;  d_h [T][hidden] bf16 out (may be d_h_out itself)
+ *   d_gamma_post, d_gamma_next  [hidden] fp32 out, over this call's tokens (T = 0: not written)
+ *   gamma_post, gamma_next, depth_n, eps and the limits as for beam_residual_boundary
+ *   workspace  device scratch of at least beam_residual_boundary_backward_workspace_bytes(T, hidden)
+ * A row of zeros with eps = 0 gives NaN, as in the forward. Equal calls give equal bits. */
+BEAM_API beam_status_t beam_residual_boundary_backward(
+    const void* y, int32_t y_dtype, const void* h_out, const float* gamma_post,
+    const float* gamma_next, const void* d_h_out, const void* d_x_next, void* d_y, void* d_h,
+    float* d_gamma_post, float* d_gamma_next, int64_t T, int32_t hidden, int32_t depth_n, float eps,
+    void* workspace, size_t workspace_bytes, void* stream);
+BEAM_API size_t beam_residual_boundary_backward_workspace_bytes(int64_t T, int32_t hidden);
+
+/* Orthogonalised update of n_mats matrices (the Muon optimiser's: the experts' momenta, or a router's):
+ * the Newton-Schulz iteration
+ *   X = G / (|G|_F + eps);  `steps` times:  A = X X^T,  X = a X + (b A + c A^2) X
+ * of each matrix by itself (along the shorter side; a zero matrix gives zeros).
+ *   g          [n_mats][rows][cols] g_dtype (BEAM_F32 or BEAM_BF16)
+ *   out        [n_mats][rows][cols] bf16
+ *   coeffs     {a, b, c} (HOST pointer, read before the call returns), each |.| <= 16
+ *   steps      >= 1
+ *   workspace  device scratch of at least beam_moe_orthogonalise_workspace_bytes(n_mats, rows, cols)
+ * The iterates are held as pairs of fp16 (about 22 bits) and the products taken on fp16 with FP32
+ * sums: before its last rounding to bf16 the result is within about 0.2% (2-norm) of the exact
+ * iteration's for coefficients that keep the singular values near 1. Iterates that grow past fp16
+ * (entries beyond 65504 / (2 sqrt(longer side))) come out infinite or NaN.
+ * Limits: rows and cols <= 65536, n_mats <= 65535, steps <= 64. Equal calls give equal bits. */
+BEAM_API beam_status_t beam_moe_orthogonalise(const void* g, int32_t g_dtype, void* out,
+                                              int64_t n_mats, int32_t rows, int32_t cols,
+                                              int32_t steps, const float* coeffs, float eps,
+                                              void* workspace, size_t workspace_bytes,
+                                              void* stream);
+BEAM_API size_t beam_moe_orthogonalise_workspace_bytes(int64_t n_mats, int32_t rows, int32_t cols);
+
 /* Dynamic FP8 E4M3 quantisation of bf16 rows, the activation step of the FP8 experts (dynamic FP8
  * checkpoints: [S] §Highlights, §BF16, NVFP4 and FP8 Model Support).
  *   src    [rows][cols] bf16 (device), cols % 8 == 0

@@ -12,6 +12,7 @@ Sources of the method (cited by tag and section in the library):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -24,7 +25,9 @@ __all__ = [
     "timing_collect", "STAGES", "status_string", "quant_fp8", "forward_routed", "dense_mlp",
     "dense_workspace_bytes", "residual_boundary", "forward_boundary", "workspace_region",
     "workspace_view", "WS_REGIONS", "convert", "dense_workspace_region", "fp8_dot_tiles",
-    "forward_noalloc",
+    "forward_noalloc", "grouped_mm", "grouped_mm_dx", "grouped_mm_dw",
+    "residual_boundary_backward", "residual_boundary_backward_workspace_bytes", "orthogonalise",
+    "orthogonalise_workspace_bytes",
 ]
 
 BEAM_F32, BEAM_BF16, BEAM_FP8_E4M3 = 0, 1, 2
@@ -120,6 +123,19 @@ def lib() -> ctypes.CDLL:
         L.beam_moe_forward_noalloc.restype = i32
         L.beam_moe_fp8_dot_tiles.argtypes = [vp, vp, vp, vp, i64, vp]
         L.beam_moe_fp8_dot_tiles.restype = i32
+        for name in ("beam_moe_grouped_mm", "beam_moe_grouped_mm_dx", "beam_moe_grouped_mm_dw"):
+            getattr(L, name).argtypes = [vp, vp, vp, vp, i64, i32, i32, i32, i32, vp]
+            getattr(L, name).restype = i32
+        L.beam_residual_boundary_backward.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                                      i64, i32, i32, f32, vp, sz, vp]
+        L.beam_residual_boundary_backward.restype = i32
+        L.beam_residual_boundary_backward_workspace_bytes.argtypes = [i64, i32]
+        L.beam_residual_boundary_backward_workspace_bytes.restype = sz
+        L.beam_moe_orthogonalise.argtypes = [vp, i32, vp, i64, i32, i32, i32,
+                                             ctypes.POINTER(f32), f32, vp, sz, vp]
+        L.beam_moe_orthogonalise.restype = i32
+        L.beam_moe_orthogonalise_workspace_bytes.argtypes = [i64, i32, i32]
+        L.beam_moe_orthogonalise_workspace_bytes.restype = sz
         L.beam_moe_convert.argtypes = [vp, i64, i32, vp, vp]
         L.beam_moe_convert.restype = i32
         _LIB = L
@@ -348,6 +364,154 @@ def fp8_dot_tiles(a, b, c, stream=None):
     if rc != 0:
         raise BeamError(rc, "beam_moe_fp8_dot_tiles")
     return d
+
+
+@contextlib.contextmanager
+def _placed(stream, *ts):
+    """Checks that the tensors (None skipped) are contiguous on one device, and makes that device and
+    the stream (default: its current one) current, so that results and workspaces allocated inside
+    belong to the stream that uses them. Yields the stream."""
+    _check_dev(*ts)
+    dev = next(t.device for t in ts if t is not None)
+    if any(t is not None and t.device != dev for t in ts):
+        raise ValueError("tensors must be on one device")
+    if stream is None:
+        with torch.cuda.device(dev):
+            yield torch.cuda.current_stream()
+    else:
+        if stream.device != dev:
+            raise ValueError("the stream is on another device than the tensors")
+        with torch.cuda.stream(stream):
+            yield stream
+
+
+def _check_tensor(name, t, shape, *dtypes):
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
+        raise ValueError(f"{name}: expected {tuple(shape)} of {' or '.join(map(str, dtypes))}, got "
+                         f"{tuple(t.shape)} of {t.dtype}")
+
+
+def _grouped(entry, a, b, offsets, R, E, N, K, shape, out, out_dtype, stream):
+    if out_dtype not in (BEAM_F32, BEAM_BF16):
+        raise BeamError(4, entry)   # BEAM_ERR_DTYPE
+    odt = torch.bfloat16 if out_dtype == BEAM_BF16 else torch.float32
+    _check_tensor("offsets", offsets, (E + 1,), torch.int32)
+    if out is not None:
+        _check_tensor("out", out, shape, odt)
+    with _placed(stream, a, b, offsets, out) as st:
+        if out is None:
+            out = torch.empty(shape, dtype=odt, device=a.device)
+        rc = getattr(lib(), entry)(_ptr(a), _ptr(b), _ptr(offsets), _ptr(out), R, E, N, K,
+                                   out_dtype, _stream(st))
+    if rc != 0:
+        raise BeamError(rc, entry)
+    return out
+
+
+def grouped_mm(x, w, offsets, out=None, out_dtype=BEAM_BF16, stream=None):
+    """beam_moe_grouped_mm: out [R][N], out[r] = x[r] . w[e]^T for the rows offsets[e] ..
+    offsets[e + 1] of expert e. x [R][K] and w [E][N][K] bf16, offsets [E + 1] int32. Rows outside
+    the offsets are left as they were (undefined when out is not given)."""
+    (R, K), (E, N, _) = x.shape, w.shape
+    _check_tensor("x", x, (R, K), torch.bfloat16)
+    _check_tensor("w", w, (E, N, K), torch.bfloat16)
+    return _grouped("beam_moe_grouped_mm", x, w, offsets, R, E, N, K, (R, N), out, out_dtype, stream)
+
+
+def grouped_mm_dx(dy, w, offsets, out=None, out_dtype=BEAM_BF16, stream=None):
+    """beam_moe_grouped_mm_dx: the gradient of grouped_mm's x, dx [R][K] with dx[r] = dy[r] . w[e],
+    from dy [R][N] bf16."""
+    (R, N), (E, _, K) = dy.shape, w.shape
+    _check_tensor("dy", dy, (R, N), torch.bfloat16)
+    _check_tensor("w", w, (E, N, K), torch.bfloat16)
+    return _grouped("beam_moe_grouped_mm_dx", dy, w, offsets, R, E, N, K, (R, K), out, out_dtype,
+                    stream)
+
+
+def grouped_mm_dw(dy, x, offsets, out=None, out_dtype=BEAM_F32, stream=None):
+    """beam_moe_grouped_mm_dw: the gradient of grouped_mm's w, dw [E][N][K] with dw[e] the sum of
+    dy[r]^T x[r] over expert e's rows (zero where it has none)."""
+    (R, N), K, E = dy.shape, x.shape[1], offsets.shape[0] - 1
+    _check_tensor("dy", dy, (R, N), torch.bfloat16)
+    _check_tensor("x", x, (R, K), torch.bfloat16)
+    return _grouped("beam_moe_grouped_mm_dw", dy, x, offsets, R, E, N, K, (E, N, K), out, out_dtype,
+                    stream)
+
+
+def residual_boundary_backward_workspace_bytes(T: int, hidden: int) -> int:
+    return int(lib().beam_residual_boundary_backward_workspace_bytes(T, hidden))
+
+
+def residual_boundary_backward(y, h_out, gamma_post, gamma_next, d_h_out, d_x_next, depth_n: int,
+                               eps: float, d_y=None, d_h=None, d_gamma_post=None,
+                               d_gamma_next=None, workspace=None, stream=None):
+    """beam_residual_boundary_backward: returns (d_y, d_h, d_gamma_post, d_gamma_next) of
+    residual_boundary's call with these y, gammas, depth_n and eps that gave h_out. d_h_out may be
+    None (no gradient through the residual stream), d_h may be d_h_out (in place)."""
+    T, H = h_out.shape
+    bf, f32 = torch.bfloat16, torch.float32
+    _check_tensor("y", y, (T, H), bf, f32)
+    for name, t in (("h_out", h_out), ("d_h_out", d_h_out), ("d_x_next", d_x_next), ("d_h", d_h)):
+        if t is not None:
+            _check_tensor(name, t, (T, H), bf)
+    for name, t in (("gamma_post", gamma_post), ("gamma_next", gamma_next),
+                    ("d_gamma_post", d_gamma_post), ("d_gamma_next", d_gamma_next)):
+        if t is not None:
+            _check_tensor(name, t, (H,), f32)
+    if d_y is not None:
+        _check_tensor("d_y", d_y, (T, H), y.dtype)
+    with _placed(stream, y, h_out, gamma_post, gamma_next, d_h_out, d_x_next, d_y, d_h, d_gamma_post,
+                 d_gamma_next, workspace) as st:
+        d_y = torch.empty_like(y) if d_y is None else d_y
+        d_h = torch.empty_like(h_out) if d_h is None else d_h
+        # no tokens: the call writes nothing, and the sums over none are zero
+        new = torch.empty if T > 0 else torch.zeros
+        if d_gamma_post is None:
+            d_gamma_post = new((H,), dtype=f32, device=y.device)
+        if d_gamma_next is None:
+            d_gamma_next = new((H,), dtype=f32, device=y.device)
+        if workspace is None:
+            nbytes = residual_boundary_backward_workspace_bytes(T, H)
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=y.device)
+        rc = lib().beam_residual_boundary_backward(
+            _ptr(y), _DT_CODE[y.dtype], _ptr(h_out), _ptr(gamma_post), _ptr(gamma_next),
+            _ptr(d_h_out), _ptr(d_x_next), _ptr(d_y), _ptr(d_h), _ptr(d_gamma_post),
+            _ptr(d_gamma_next), T, H, int(depth_n), float(eps), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(st))
+    if rc != 0:
+        raise BeamError(rc, "beam_residual_boundary_backward")
+    return d_y, d_h, d_gamma_post, d_gamma_next
+
+
+def orthogonalise_workspace_bytes(n_mats: int, rows: int, cols: int) -> int:
+    return int(lib().beam_moe_orthogonalise_workspace_bytes(n_mats, rows, cols))
+
+
+def orthogonalise(g, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, out=None,
+                  workspace=None, stream=None):
+    """beam_moe_orthogonalise: the Newton-Schulz iterate of each matrix of g ([n][rows][cols], or one
+    [rows][cols]; bf16 or fp32), as bf16. The default coefficients and steps are the Muon optimiser's."""
+    if g.dim() not in (2, 3):
+        raise ValueError("g: expected [rows][cols] or [n][rows][cols]")
+    rows, cols = g.shape[-2:]
+    n = g.shape[0] if g.dim() == 3 else 1
+    _check_tensor("g", g, g.shape, torch.bfloat16, torch.float32)
+    if out is not None:
+        _check_tensor("out", out, g.shape, torch.bfloat16)
+    abc = (ctypes.c_float * 3)(*[float(c) for c in coeffs])
+    with _placed(stream, g, out, workspace) as st:
+        if out is None:
+            out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+        if workspace is None:
+            nbytes = orthogonalise_workspace_bytes(n, rows, cols)
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=g.device)
+        rc = lib().beam_moe_orthogonalise(_ptr(g), _DT_CODE[g.dtype], _ptr(out), n, rows, cols,
+                                          int(steps), abc, float(eps), _ptr(workspace),
+                                          workspace.numel() * workspace.element_size(),
+                                          _stream(st))
+    if rc != 0:
+        raise BeamError(rc, "beam_moe_orthogonalise")
+    return out
 
 
 WS_REGIONS = {"expert_off": 0, "sorted_slot": 1, "h": 2, "hq": 3, "hs": 4, "xq": 5, "xs": 6,

@@ -143,4 +143,47 @@ hipError_t launch_boundary(const BoundaryArgs& b, const float* Y, int K, const i
                            hipStream_t st);
 hipError_t launch_combine(const float* ybuf, void* out, bool out_bf16, const Shape& s,
                           const int32_t* ids, int e_begin, int e_end, hipStream_t st);
+
+// ---- training operators ----
+// out[r][0 .. No) = a[r] . w[expert of r] for rows grouped by `offsets`; w_across: w is [E][Kc][No]
+// (its rows run across the contraction), else [E][No][Kc].
+hipError_t launch_grouped_rows(const void* a, const void* w, const int32_t* offsets, void* out,
+                               int R, int E, int No, int Kc, bool w_across, bool out_bf16,
+                               hipStream_t st);
+// dw[e] [N][K] = dy_e^T x_e
+hipError_t launch_grouped_dw(const void* dy, const void* x, const int32_t* offsets, void* dw, int R,
+                             int E, int N, int K, bool out_bf16, hipStream_t st);
+// Bound on a grouped launch: its workgroups are counted in 32 bits.
+bool grouped_grid_fits(int64_t R, int64_t E, int64_t N, int64_t K);
+
+struct BoundaryBwdArgs {
+  const void* y;             // [T][H] the forward's y
+  bool y_bf16;
+  const uint16_t* h;         // [T][H] the forward's h_out
+  const float* gamma_post;   // [H]
+  const float* gamma_next;   // [H]
+  const uint16_t* d_h_in;    // [T][H] gradient of h_out (nullable)
+  const uint16_t* d_x;       // [T][H] gradient of x_next
+  void* d_y;                 // [T][H] in y's type
+  uint16_t* d_h;             // [T][H] (may be d_h_in)
+  float* d_gamma_post;       // [H]
+  float* d_gamma_next;       // [H]
+  float* parts;              // [boundary_bwd_parts(T)][2][H]
+  float alpha, beta, eps;
+};
+int boundary_bwd_parts(int64_t T);
+hipError_t launch_boundary_bwd(const BoundaryBwdArgs& a, int64_t T, int H, hipStream_t st);
+
+// Workspace of the orthogonalised update (byte offsets): partial sums of squares, X as hi (two, in
+// turn) + lo, A and B; m <= n its sides, mp and ld their padded row lengths.
+struct NsLayout {
+  size_t parts = 0, hi[2] = {0, 0}, lo = 0, gram = 0, poly = 0, total = 0;
+  int m = 0, n = 0, mp = 0, ld = 0;
+  bool tall = false;
+};
+NsLayout ns_layout(int64_t n_mats, int rows, int cols);
+bool ns_grid_fits(int64_t n_mats, int rows, int cols);
+hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n_mats, int rows,
+                                int cols, int steps, const float* coeffs, float eps, char* ws,
+                                hipStream_t st);
 }  // namespace beam
