@@ -5,10 +5,11 @@
 // (each row a run of k: "row" operands) or across it (each row one k, a run of m or n: "column"
 // operands), so the four products Y = X W^T, dX = dY W, dW = dY^T X and X X^T all read their operands
 // where they lie, without a transposed copy.
-//   * A stage carries 64 values of k. Both kinds reach LDS by 16-byte direct loads, 1 KB a wave
+//   * A stage carries 64 values of k (or 32, two column operands). Both kinds reach LDS by 16-byte direct loads, 1 KB a wave
 //     instruction. Row operands: [rows][64 k], chunk c of row r at c ^ (r & 7), fragments by 16-byte
-//     reads (8 consecutive k of one row). Column operands: [64 k][rows], the 32-byte unit u of row k
-//     at u ^ f(k), f = (k & 3) | (k >> 3 & 1) << 2, fragments by transposing 8-byte reads
+//     reads (8 consecutive k of one row). Column operands: [k][rows], the 32-byte unit u of row k
+//     at u ^ f(k), f = (k & 3) | (k >> 3 & 1) << 2 (64 rows: its upper two bits, two stored rows being
+//     256 bytes), fragments by transposing 8-byte reads
 //     (ds_read_b64_tr_b16: 16 lanes hand in 4 rows x 16 columns and take a column each); the eight
 //     rows that half a wave touches lie on distinct banks.
 //   * Past an operand's rows, or past k, loads fall outside their buffer and leave zeros in LDS, so
@@ -26,19 +27,31 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-constexpr int kTileK = 64;   // values of k in a stage (128 bytes)
-
-// Workgroup tile of BM x BN, WM x WN waves, ST stages of LDS.
-template <int BM_, int BN_, int WM_, int WN_, int ST_>
+// Workgroup tile of BM x BN, WM x WN waves; LDS rings of AST stages of the A operand and BST of B
+// (AST <= BST: B is the one that streams from HBM, A's rows are shared by neighbouring tiles), of KT
+// values of k each.
+template <int BM_, int BN_, int WM_, int WN_, int AST_, int BST_, int KT_ = 64>
 struct TileShape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, AST = AST_, BST = BST_, KT = KT_;
+  static_assert(KT == 32 || KT == 64, "a row operand's swizzle is made for 64");
+  static_assert(2 <= AST && AST <= BST, "ring depths");
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int FM = BM / 16 / WM, FN = BN / 16 / WN;   // 16 x 16 sub-tiles of a wave
-  static constexpr int kABytes = BM * 2 * kTileK, kBBytes = BN * 2 * kTileK;
-  static constexpr int kLdsBytes = ST * (kABytes + kBBytes);
+  static constexpr int kABytes = BM * 2 * KT, kBBytes = BN * 2 * KT;
+  static constexpr int kLdsBytes = AST * kABytes + BST * kBBytes;
   static_assert(kLdsBytes <= 160 * 1024, "LDS budget");
   static_assert(FM * 16 * WM == BM && FN * 16 * WN == BN, "whole sub-tiles");
 };
+
+// Wave-uniform values that the compiler would otherwise keep in vector registers, where a buffer
+// descriptor made from them costs a loop around every load.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+template <class T>
+__device__ __forceinline__ T* uniform(T* p) {
+  const uint64_t u = (uint64_t)p;
+  return (T*)((uint64_t)(uint32_t)uniform((int)(uint32_t)u) |
+              (uint64_t)(uint32_t)uniform((int)(uint32_t)(u >> 32)) << 32);
+}
 
 // One operand of a tile, wave-uniform.
 struct TileOperand {
@@ -48,16 +61,24 @@ struct TileOperand {
   int32_t tail;                // column operands: bytes from base to the end of its own row
 };
 
+// f(k) of a column operand, from k & 3 and bit 3 of k
+template <int ROWS>
+__device__ __forceinline__ int column_swizzle(int low, int bit3) {
+  return ROWS >= 128 ? low | bit3 << 2 : low >> 1 | bit3 << 1;
+}
+
 // Direct loads of one operand's stages (ROWS = BM or BN).
-template <int ROWS, int WAVES, bool COL>
+template <int ROWS, int WAVES, bool COL, int KT>
 struct OperandLoader {
-  static constexpr int L = ROWS / 8 / WAVES;   // 1 KB loads of a wave in a stage
-  static_assert(L * 8 * WAVES == ROWS, "loads split evenly over waves");
+  static constexpr int L = ROWS * KT / 512 / WAVES;   // 1 KB loads of a wave in a stage
+  static_assert(L * 512 * WAVES == ROWS * KT, "loads split evenly over waves");
+  static_assert(COL || KT == 64, "the swizzle of row operands is made for 128-byte rows");
   static constexpr int kRowChunks = COL ? ROWS / 8 : 8;       // 16-byte chunks of a stored row
   static constexpr int kLoadRows = 64 / kRowChunks;           // stored rows of a load
-  static_assert(!COL || ROWS >= 128, "the swizzle needs eight 32-byte units a row");
+  static_assert(!COL || ROWS >= 64, "the swizzle needs four 32-byte units a row");
   TileOperand op;
   uint32_t voff[L];
+  bool stream = false;   // read once: non-temporal loads
   int kofs;   // row operands: first k of this lane's chunk within a stage
 
   __device__ __forceinline__ void init(const TileOperand& o, int wave, int lane) {
@@ -68,7 +89,7 @@ struct OperandLoader {
     for (int q = 0; q < L; ++q) {
       const int row = (wave * L + q) * kLoadRows + lr;
       if constexpr (COL) {
-        const int f = (row & 3) | ((row >> 1) & 4);
+        const int f = column_swizzle<ROWS>(row & 3, (row >> 3) & 1);
         voff[q] = (uint32_t)(row * op.ld + (slot ^ (f << 1)) * 16);
       } else {
         voff[q] = (uint32_t)(row * op.ld + kofs * 2);
@@ -78,21 +99,29 @@ struct OperandLoader {
 
   // stage kt of a contraction over k values into the LDS ring slot at dst
   __device__ __forceinline__ void issue(int kt, int64_t k, unsigned char* dst, int wave) const {
+    if (stream)
+      issue_as<kCachePolicyNT>(kt, k, dst, wave);
+    else
+      issue_as<0>(kt, k, dst, wave);
+  }
+  template <int kAux>
+  __device__ __forceinline__ void issue_as(int kt, int64_t k, unsigned char* dst, int wave) const {
     if constexpr (COL) {
-      const int64_t left = k - (int64_t)kt * kTileK;
-      const int rows = left < kTileK ? (int)left : kTileK;
-      const unsigned char* base = op.base + (int64_t)kt * kTileK * op.ld;
-      const uint32_t bytes = rows > 0 ? (uint32_t)((rows - 1) * op.ld + op.tail) : 0u;
+      const int64_t left = k - (int64_t)kt * KT;
+      const int rows = left < KT ? (int)left : KT;
+      const unsigned char* base = uniform(op.base + (int64_t)kt * KT * op.ld);
+      const uint32_t bytes =
+          (uint32_t)uniform(rows > 0 ? (int)((rows - 1) * op.ld + op.tail) : 0);
 #pragma unroll
       for (int q = 0; q < L; ++q)
-        buffer_load_lds16<0>(base, bytes, voff[q], 0, (lds_void_t*)(dst + (wave * L + q) * 1024));
+        buffer_load_lds16<kAux>(base, bytes, voff[q], 0, (lds_void_t*)(dst + (wave * L + q) * 1024));
     } else {
       const uint32_t bytes = (uint32_t)(op.rows * op.ld);
       // chunks past k: an offset past every buffer (a tile's rows are under 2 GiB)
-      const uint32_t past = (int64_t)kt * kTileK + kofs < k ? 0u : 0x80000000u;
+      const uint32_t past = (int64_t)kt * KT + kofs < k ? 0u : 0x80000000u;
 #pragma unroll
       for (int q = 0; q < L; ++q)
-        buffer_load_lds16<0>(op.base, bytes, voff[q] | past, (uint32_t)kt * (2 * kTileK),
+        buffer_load_lds16<kAux>(op.base, bytes, voff[q] | past, (uint32_t)kt * (2 * KT),
                              (lds_void_t*)(dst + (wave * L + q) * 1024));
     }
   }
@@ -108,7 +137,7 @@ struct FragReader {
   __device__ __forceinline__ void init(int first, int lane) {
     const int r = lane & 15, g = lane >> 4;
     if constexpr (COL) {
-      const int f = (r >> 2) | ((g & 1) << 2);
+      const int f = column_swizzle<ROWS>(r >> 2, g & 1);
 #pragma unroll
       for (int i = 0; i < COUNT; ++i)
         off[i] = (8 * g + (r >> 2)) * (2 * ROWS) + (r & 3) * 8 + (((first + STEP * i) ^ f) << 5);
@@ -118,7 +147,9 @@ struct FragReader {
         off[s] = first * 2048 + r * 128 + (((4 * s + g) ^ (r & 7)) << 4);
     }
   }
-  __device__ __forceinline__ intx4 read(const unsigned char* slot, int i, int s) const {
+  // __restrict__: without it the compiler takes a transposing read to alias the direct loads in flight
+  // and waits for all of them first (vmcnt 0 in every stage; the input gradient ran 20% slower)
+  __device__ __forceinline__ intx4 read(const unsigned char* __restrict__ slot, int i, int s) const {
     if constexpr (COL) {
       const unsigned char* p = slot + s * (32 * 2 * ROWS) + off[i];
       const u32x2 lo = __builtin_bit_cast(
@@ -149,57 +180,126 @@ __device__ __forceinline__ void tile_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// The loop over k of one tile. acc[i][j] is sub-tile (wm + WM i, wn FN + j); NV of the wave's FM row
-// sub-tiles hold rows, the others' accumulators are left alone.
+// One wave's side of a stage: its fragments and their schedule. A stage is NV positions a step: position p
+// multiplies row sub-tile p % NV in step p / NV; acc[i][j] is sub-tile (wm + WM i, wn FN + j). NV of
+// the wave's FM row sub-tiles hold rows, the others' accumulators are left alone.
+//
+// Fragments are read ahead of their MFMAs, the row operand's AHEAD positions, the other's one step.
+// Once the last AHEAD positions' fragments of a stage are in registers, its slot is free: there, and
+// not at the stage's end, stands its one barrier (`turn`), so the reads of the next stage run under
+// this one's last MFMAs.
 template <class S, bool ACOL, bool BCOL, bool F16, int NV>
-__device__ __forceinline__ void tile_kloop(const OperandLoader<S::BM, S::kWaves, ACOL>& la,
-                                           const OperandLoader<S::BN, S::kWaves, BCOL>& lb,
-                                           int64_t k, unsigned char* smem, int wave, int lane,
-                                           floatx4 (&acc)[S::FM][S::FN]) {
+struct TileStage {
+  static constexpr int STEPS = S::KT / 32, P = STEPS * NV, AHEAD = NV < 4 ? NV : 4;
   FragReader<S::BM, NV, S::WM, ACOL> ra;
   FragReader<S::BN, S::FN, 1, BCOL> rb;
-  ra.init(wave / S::WN, lane);
-  rb.init(wave % S::WN * S::FN, lane);
-  const int nk = (int)((k + kTileK - 1) / kTileK);
+  intx4 af[P + AHEAD], bf[STEPS + 1][S::FN];   // the next stage's first ones at the end
+
+  __device__ __forceinline__ void init(int wave, int lane) {
+    ra.init(wave / S::WN, lane);
+    rb.init(wave % S::WN * S::FN, lane);
+  }
+  // the first fragments of the first stage, which has landed in the slots sa, sb
+  __device__ __forceinline__ void start(const unsigned char* sa, const unsigned char* sb) {
+#pragma unroll
+    for (int j = 0; j < S::FN; ++j) bf[0][j] = rb.read(sb, j, 0);
+#pragma unroll
+    for (int p = 0; p < AHEAD; ++p) af[p] = ra.read(sa, p, 0);
+  }
+  // multiplies the stage in sa, sb; `turn` waits until the next one has landed in na, nb (behind the
+  // last stage the fragments read from there are not used) and issues further loads
+  template <class Turn>
+  __device__ __forceinline__ void run(const unsigned char* sa, const unsigned char* sb,
+                                      const unsigned char* na, const unsigned char* nb, Turn&& turn,
+                                      floatx4 (&acc)[S::FM][S::FN]) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int s = p / NV;
+      if (p == P - AHEAD) turn();
+      if (p + AHEAD < P)
+        af[p + AHEAD] = ra.read(sa, (p + AHEAD) % NV, (p + AHEAD) / NV);
+      else
+        af[p + AHEAD] = ra.read(na, (p + AHEAD) % NV, (p + AHEAD - P) / NV);
+      // the other operand's next step, spread over the last positions of this one
+      constexpr int kBEach = (S::FN + AHEAD - 1) / AHEAD;
+      const int q = p % NV - (NV - AHEAD);
+      if (q >= 0) {
+#pragma unroll
+        for (int j = q * kBEach; j < (q + 1) * kBEach && j < S::FN; ++j) {
+          if (s + 1 < STEPS)
+            bf[s + 1][j] = rb.read(sb, j, s + 1);
+          else
+            bf[STEPS][j] = rb.read(nb, j, 0);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j)
+        acc[p % NV][j] = tile_mma<F16>(bf[s][j], af[p], acc[p % NV][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int j = 0; j < S::FN; ++j) bf[0][j] = bf[STEPS][j];
+#pragma unroll
+    for (int p = 0; p < AHEAD; ++p) af[p] = af[P + p];
+  }
+};
+
+template <class S>
+__device__ __forceinline__ void tile_zero(floatx4 (&acc)[S::FM][S::FN]) {
+#pragma unroll
+  for (int i = 0; i < S::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < S::FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+}
+
+// The loop over k of one tile.
+template <class S, bool ACOL, bool BCOL, bool F16, int NV>
+__device__ __forceinline__ void tile_kloop(const OperandLoader<S::BM, S::kWaves, ACOL, S::KT>& la,
+                                           const OperandLoader<S::BN, S::kWaves, BCOL, S::KT>& lb,
+                                           int64_t k, unsigned char* smem, int wave, int lane,
+                                           floatx4 (&acc)[S::FM][S::FN]) {
+  const int nk = (int)((k + S::KT - 1) / S::KT);
+  if (nk == 0) return;
   unsigned char* const aring = smem;
-  unsigned char* const bring = smem + S::ST * S::kABytes;
-  constexpr int kPerStage = OperandLoader<S::BM, S::kWaves, ACOL>::L +
-                            OperandLoader<S::BN, S::kWaves, BCOL>::L;
-  static_assert((S::ST - 1) * kPerStage < 64, "vmcnt range");
+  unsigned char* const bring = smem + S::AST * S::kABytes;
+  constexpr int LA = OperandLoader<S::BM, S::kWaves, ACOL, S::KT>::L;
+  constexpr int LB = OperandLoader<S::BN, S::kWaves, BCOL, S::KT>::L;
+  static_assert(S::BST * (LA + LB) < 64, "vmcnt range");
+  // a wave's loads are issued, and counted, in the order A(t), B(t + BST - AST)
+  auto issue_a = [&](int st) { la.issue(st, k, aring + (st % S::AST) * S::kABytes, wave); };
+  auto issue_b = [&](int st) { lb.issue(st, k, bring + (st % S::BST) * S::kBBytes, wave); };
 #pragma unroll
-  for (int p = 0; p < S::ST - 1; ++p)
-    if (p < nk) {
-      la.issue(p, k, aring + p * S::kABytes, wave);
-      lb.issue(p, k, bring + p * S::kBBytes, wave);
-    }
+  for (int p = 0; p < S::BST; ++p) {
+    if (p < S::AST && p < nk) issue_a(p);
+    if (p < nk) issue_b(p);
+  }
+  if (nk >= S::BST)
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm((S::AST - 1) * LA + (S::BST - 1) * LB));
+  else
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+  tile_barrier();
+  TileStage<S, ACOL, BCOL, F16, NV> stage;
+  stage.init(wave, lane);
+  stage.start(aring, bring);
+  int ia = 0, ib = 0;   // ring slots of the stage
   for (int kt = 0; kt < nk; ++kt) {
-    // the wave's own loads of stage kt have landed; after the barrier everyone's have, and everyone
-    // is done reading the slot that stage kt + ST - 1 takes
-    if (kt + S::ST - 2 < nk)
-      __builtin_amdgcn_s_waitcnt(vmcnt_imm((S::ST - 2) * kPerStage));
-    else
-      __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-    tile_barrier();
-    const int nx = kt + S::ST - 1;
-    if (nx < nk) {
-      la.issue(nx, k, aring + (nx % S::ST) * S::kABytes, wave);
-      lb.issue(nx, k, bring + (nx % S::ST) * S::kBBytes, wave);
-    }
-    const unsigned char* sa = aring + (kt % S::ST) * S::kABytes;
-    const unsigned char* sb = bring + (kt % S::ST) * S::kBBytes;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      intx4 bf[S::FN], af[NV];
-#pragma unroll
-      for (int j = 0; j < S::FN; ++j) bf[j] = rb.read(sb, j, s);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) af[i] = ra.read(sa, i, s);
-      __builtin_amdgcn_sched_barrier(0);   // all reads ahead of the MFMA chain
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < S::FN; ++j) acc[i][j] = tile_mma<F16>(bf[j], af[i], acc[i][j]);
-    }
+    const int ja = ia + 1 == S::AST ? 0 : ia + 1, jb = ib + 1 == S::BST ? 0 : ib + 1;
+    stage.run(aring + ia * S::kABytes, bring + ib * S::kBBytes, aring + ja * S::kABytes,
+              bring + jb * S::kBBytes,
+              [&]() {
+                // own reads of this stage are done; own loads of the next one have landed
+                if (kt + S::BST <= nk)
+                  __builtin_amdgcn_s_waitcnt(
+                      vmcnt_imm((S::AST - 2) * LA + (S::BST - 2) * LB) & kLgkmZero);
+                else
+                  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0) & kLgkmZero);
+                tile_barrier();
+                if (kt + S::AST < nk) la.issue(kt + S::AST, k, aring + ia * S::kABytes, wave);
+                if (kt + S::BST < nk) lb.issue(kt + S::BST, k, bring + ib * S::kBBytes, wave);
+              },
+              acc);
+    ia = ja;
+    ib = jb;
   }
 }
 
@@ -215,16 +315,54 @@ __device__ __forceinline__ void tile_for_each(const floatx4 (&acc)[S::FM][S::FN]
         16 * (wave % S::WN * S::FN + j) + 4 * (lane >> 4), acc[i][j]);
 }
 
-// Four consecutive values to bf16 or fp32 at element offset `at` (8- or 16-byte aligned).
-template <bool OUT_BF16>
-__device__ __forceinline__ void store4(void* out, int64_t at, floatx4 v) {
-  if constexpr (OUT_BF16) {
-    u32x2 o;
-    o.x = f32_to_bf16_bits(v.x) | (f32_to_bf16_bits(v.y) << 16);
-    o.y = f32_to_bf16_bits(v.z) | (f32_to_bf16_bits(v.w) << 16);
-    *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(out) + at) = o;
-  } else {
-    *reinterpret_cast<floatx4*>(reinterpret_cast<float*>(out) + at) = v;
+// Two values rounded to bf16, to nearest even, by one conversion instruction.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
+
+// Stores a tile's accumulators (NV row sub-tiles a wave): rows m < rows and columns n < cols, cols a
+// multiple of 8, of the tile whose first value is at `out`, `ld` bytes from row to row (a tile's
+// rows under 2 GiB). An instruction writes 64 bytes of each of 16 rows in 16-byte pieces; for bf16
+// that takes two neighbouring sub-tiles, whose halves a lane swaps with the lane 16 away (64-byte
+// runs of plain stores fill memory at 5.4 TB/s, the 32-byte runs of one bf16 sub-tile at 4.4;
+// non-temporal stores of less than whole lines at 2 - 3). Lanes outside are dropped by the buffer's
+// bounds.
+template <class S, int NV, bool OUT_BF16>
+__device__ __forceinline__ void tile_store(const floatx4 (&acc)[S::FM][S::FN], void* out, int64_t ld,
+                                           int rows, int cols, int wave, int lane) {
+  static_assert(S::FN % 2 == 0, "sub-tiles in pairs");
+  constexpr int kSize = OUT_BF16 ? 2 : 4;
+  const int m0 = 16 * (wave / S::WN) + (lane & 15), g = lane >> 4;
+  // bf16: lanes g = 0, 2 take columns 0-7, 8-15 of the pair's first sub-tile, g = 1, 3 of its second
+  const int n0 = 16 * (wave % S::WN * S::FN) + (OUT_BF16 ? 16 * (g & 1) + 4 * (g & 2) : 4 * g);
+  const uint32_t bytes = (uint32_t)((min(rows, S::BM) - 1) * ld + min(cols, S::BN) * kSize);
+  const auto rsrc =
+      __builtin_amdgcn_make_buffer_rsrc(uniform(out), (short)0, uniform((int)bytes), 0x00020000);
+  const uint32_t v0 = (uint32_t)(m0 * ld + n0 * kSize);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const bool in_row = m0 + 16 * S::WM * i < rows;
+    const uint32_t row = (uint32_t)(16 * S::WM * i * ld);
+#pragma unroll
+    for (int j = 0; j < S::FN; j += OUT_BF16 ? 2 : 1) {
+      // outside: past the buffer whichever way its range check counts the scalar offset
+      const uint32_t voff = in_row && n0 + 16 * j < cols ? v0 : 0x80000000u;
+      const uint32_t soff = row + 16 * j * kSize;
+      u32x4 o;
+      if constexpr (OUT_BF16) {
+        const floatx4 v = acc[i][j], w = acc[i][j + 1];
+        const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16(v.x, v.y), pack_bf16(w.x, w.y),
+                                                        false, false);
+        const auto y = __builtin_amdgcn_permlane16_swap(pack_bf16(v.z, v.w), pack_bf16(w.z, w.w),
+                                                        false, false);
+        o = u32x4{x[0], y[0], x[1], y[1]};
+      } else {
+        o = __builtin_bit_cast(u32x4, acc[i][j]);
+      }
+      __builtin_amdgcn_raw_buffer_store_b128(o, rsrc, voff, soff, 0);
+    }
   }
 }
 

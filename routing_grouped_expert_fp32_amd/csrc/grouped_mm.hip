@@ -14,6 +14,7 @@
 // Workgroup L runs on XCD L % 8, so the tiles are cut into 8 contiguous runs, one per XCD, whose
 // neighbours share operands in that XCD's L2.
 #include <algorithm>
+#include <type_traits>
 
 #include "gemm_tile.h"
 
@@ -110,7 +111,7 @@ constexpr int kTileGroup = 4;   // blocks of one expert walked together, column 
 template <class S, bool WCOL, bool OUT_BF16>
 __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) void grouped_rows_kernel(
     const unsigned char* __restrict__ a, const unsigned char* __restrict__ w,
-    const int32_t* __restrict__ offsets, void* __restrict__ out, int R, int E, int No, int Kc,
+    const int32_t* __restrict__ offsets, unsigned char* __restrict__ out, int R, int E, int No, int Kc,
     int n_ctiles, int max_blocks) {
   __shared__ __attribute__((aligned(16))) unsigned char smem[S::kLdsBytes];
   const int lane = threadIdx.x & 63;
@@ -138,8 +139,9 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   const int col0 = ctile * S::BN;
   const int64_t wbytes = (int64_t)No * Kc * 2;
   const int64_t a_ld = (int64_t)Kc * 2;
-  OperandLoader<S::BM, S::kWaves, false> la;
-  OperandLoader<S::BN, S::kWaves, WCOL> lb;
+  OperandLoader<S::BM, S::kWaves, false, S::KT> la;
+  OperandLoader<S::BN, S::kWaves, WCOL, S::KT> lb;
+  lb.stream = blk.n_blocks == 1;   // weights that no other block reads need not stay in L2
   la.init({a + (int64_t)blk.row0 * a_ld, a_ld, blk.rows, 0}, wave, lane);
   if constexpr (WCOL)
     lb.init({w + blk.e * wbytes + (int64_t)col0 * 2, (int64_t)No * 2, 0, (No - col0) * 2}, wave,
@@ -148,103 +150,173 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
     lb.init({w + blk.e * wbytes + (int64_t)col0 * a_ld, a_ld, min(S::BN, No - col0), 0}, wave, lane);
 
   floatx4 acc[S::FM][S::FN];
-#pragma unroll
-  for (int i = 0; i < S::FM; ++i)
-#pragma unroll
-    for (int j = 0; j < S::FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+  tile_zero<S>(acc);
 
-  auto store = [&](int m, int n, floatx4 d) {
-    if (m < blk.rows && col0 + n < No)   // No % 8 == 0: four columns are all in or all out
-      store4<OUT_BF16>(out, (int64_t)(blk.row0 + m) * No + col0 + n, d);
+  // sub-tiles of 16 rows are dealt to the wave rows in turn; a wave runs the body for the number it
+  // has, in steps of two, so a partly filled block costs about its rows
+  const int nsub = (blk.rows + 15) >> 4, wm = wave / S::WN;
+  const int nv = (nsub - wm + S::WM - 1) / S::WM;   // wave-uniform; 0 where nsub <= wm
+  auto body = [&](auto nv_tag) {
+    constexpr int NV = decltype(nv_tag)::value;
+    tile_kloop<S, false, WCOL, false, NV>(la, lb, Kc, smem, wave, lane, acc);
+    constexpr int kSize = OUT_BF16 ? 2 : 4;
+    tile_store<S, NV, OUT_BF16>(acc, out + ((int64_t)blk.row0 * No + col0) * kSize,
+                                (int64_t)No * kSize, blk.rows, No - col0, wave, lane);
   };
-  tile_kloop<S, false, WCOL, false, S::FM>(la, lb, Kc, smem, wave, lane, acc);
-  tile_for_each<S, S::FM>(acc, wave, lane, store);
+  if (S::FM > 8 && nv > 8)
+    body(std::integral_constant<int, S::FM>{});
+  else if (S::FM > 6 && nv > 6)
+    body(std::integral_constant<int, S::FM < 8 ? S::FM : 8>{});
+  else if (S::FM > 4 && nv > 4)
+    body(std::integral_constant<int, S::FM < 6 ? S::FM : 6>{});
+  else if (S::FM > 2 && nv > 2)
+    body(std::integral_constant<int, S::FM < 4 ? S::FM : 4>{});
+  else
+    body(std::integral_constant<int, 2>{});
 }
 
 // dw[e] (N x K) = dy_e^T x_e: both operands lie across the contraction (the expert's rows).
+//
+// Each expert's tiles are cut into 8 runs, one per XCD, so an expert with many rows loads all XCDs
+// alike (experts dealt to XCDs whole: 4.36 ms instead of 2.07 at 32768 rows, two of 32 experts with
+// 40% of them, 5120 x 5120 gradients in fp32).
 template <class S, bool OUT_BF16>
 __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) void grouped_dw_kernel(
     const unsigned char* __restrict__ dy, const unsigned char* __restrict__ x,
-    const int32_t* __restrict__ offsets, void* __restrict__ dw, int R, int E, int N, int K,
+    const int32_t* __restrict__ offsets, unsigned char* __restrict__ dw, int R, int E, int N, int K,
     int n_mtiles, int n_ctiles) {
   __shared__ __attribute__((aligned(16))) unsigned char smem[S::kLdsBytes];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int v = xcd_tile(blockIdx.x, E * n_mtiles * n_ctiles);
-  if (v < 0) return;
-  const int per = n_mtiles * n_ctiles, e = v / per, t = v % per;
+  const int per = n_mtiles * n_ctiles, run = (per + 7) >> 3;
+  const int local = blockIdx.x >> 3, e = local / run;
+  const int t = (blockIdx.x & 7) * run + local % run;
+  if (e >= E || t >= per) return;
   // tiles of one matrix in bands of kTileGroup tile rows, column by column
-  const int band = t / (kTileGroup * n_ctiles), m0 = band * kTileGroup;
+  const int m0 = t / (kTileGroup * n_ctiles) * kTileGroup;
   const int sz = min(kTileGroup, n_mtiles - m0), at = t - m0 * n_ctiles;
   const int row0 = (m0 + at % sz) * S::BM, col0 = at / sz * S::BN;
   int begin, end;
   expert_rows(offsets, e, R, begin, end);
-  OperandLoader<S::BM, S::kWaves, true> la;
-  OperandLoader<S::BN, S::kWaves, true> lb;
-  la.init({dy + (int64_t)begin * N * 2 + (int64_t)row0 * 2, (int64_t)N * 2, 0, (N - row0) * 2},
-          wave, lane);
-  lb.init({x + (int64_t)begin * K * 2 + (int64_t)col0 * 2, (int64_t)K * 2, 0, (K - col0) * 2},
-          wave, lane);
+  const int64_t a_ld = (int64_t)N * 2, b_ld = (int64_t)K * 2;
+  OperandLoader<S::BM, S::kWaves, true, S::KT> la;
+  OperandLoader<S::BN, S::kWaves, true, S::KT> lb;
+  la.init({dy + begin * a_ld + (int64_t)row0 * 2, a_ld, 0, (N - row0) * 2}, wave, lane);
+  lb.init({x + begin * b_ld + (int64_t)col0 * 2, b_ld, 0, (K - col0) * 2}, wave, lane);
   floatx4 acc[S::FM][S::FN];
-#pragma unroll
-  for (int i = 0; i < S::FM; ++i)
-#pragma unroll
-    for (int j = 0; j < S::FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+  tile_zero<S>(acc);
   tile_kloop<S, true, true, false, S::FM>(la, lb, end - begin, smem, wave, lane, acc);
-  tile_for_each<S, S::FM>(acc, wave, lane, [&](int m, int n, floatx4 d) {
-    if (row0 + m < N && col0 + n < K)
-      store4<OUT_BF16>(dw, ((int64_t)e * N + row0 + m) * K + col0 + n, d);
-  });
+  constexpr int kSize = OUT_BF16 ? 2 : 4;
+  tile_store<S, S::FM, OUT_BF16>(acc, dw + (((int64_t)e * N + row0) * K + col0) * kSize,
+                                 (int64_t)K * kSize, N - row0, K - col0, wave, lane);
 }
 
-using TileLarge = TileShape<256, 256, 2, 4, 2>;
-using TileSmall = TileShape<128, 128, 2, 2, 2>;
+// Tiles of the forward and the input gradient, by the mean number of rows of an expert (the counts
+// themselves are on the device). Measured at 32 experts of 5120 x 5120 (us, forward; a 1.68 GB read
+// of the weights alone takes about 260):
+//   rows / expert         1    64   110   156   256
+//   32 x 128  (4, 4)    173    443
+//   128 x 256 (2, 3)           308   324   433
+//   192 x 256 (2, 3)           311   323   350
+//   320 x 256 (2, 2)           381   384   396   447
+//   256 x 256 (2, 2)                               564
+// Few rows: narrow tiles, many workgroups streaming weights. More: one block an expert if it can be,
+// as every further block reads the weights again; the B operand's third stage covers their latency
+// while LDS lasts. Past 1536 rows blocks are many anyway and 256 x 256 multiplies fastest (one
+// matrix of 8192 x 8192, 8192 rows: 794 us, 320 x 256 895). Where a tile leaves CUs without work,
+// 64 x 64: 523 rows, 16 experts of 776 x 520, 6.9 us (128 x 128 tiles 12.3).
+using TileStream = TileShape<32, 128, 1, 4, 4, 4>;
+using Tile64 = TileShape<64, 64, 1, 2, 3, 3>;
+using Tile128 = TileShape<128, 256, 2, 4, 2, 3>;
+using Tile192 = TileShape<192, 256, 2, 4, 2, 3>;
+using Tile256 = TileShape<256, 256, 2, 4, 2, 2>;
+using Tile320 = TileShape<320, 256, 2, 4, 2, 2>;
+constexpr int kGroupedCus = 256;
+
+template <class F>
+static void with_rows_tile(int64_t R, int64_t E, int64_t No, F&& f) {
+  const int64_t mean = ceil_div(R, E), full = std::min(R, E);
+  auto fits = [&](int64_t bm, int64_t bn) {
+    return full * ceil_div(mean, bm) * ceil_div(No, bn) >= kGroupedCus;
+  };
+  if (mean <= 24 && fits(32, 128))
+    f(TileStream{});
+  else if (mean <= 112 && fits(128, 256))
+    f(Tile128{});
+  else if (mean <= 192 && fits(192, 256))
+    f(Tile192{});
+  else if (mean <= 1536 && fits(320, 256))
+    f(Tile320{});
+  else if (fits(256, 256))
+    f(Tile256{});
+  else
+    f(Tile64{});
+}
+
+// Blocks that R rows of E experts can make.
+static int64_t max_blocks(int64_t R, int64_t E, int64_t bm) { return R / bm + std::min(R, E) + 1; }
 
 bool grouped_grid_fits(int64_t R, int64_t E, int64_t N, int64_t K) {
-  const int64_t blocks = R / 128 + std::min(R, E) + 1;
-  const int64_t nt = ceil_div(N, 128), kt = ceil_div(K, 128), lim = (int64_t(1) << 31) - 8;
-  return blocks * std::max(nt, kt) < lim && E * nt * kt < lim;
-}
-
-template <class S, bool WCOL>
-static void launch_rows(const void* a, const void* w, const int32_t* offsets, void* out, int R,
-                        int E, int No, int Kc, bool out_bf16, hipStream_t st) {
-  const int64_t blocks = R / S::BM + std::min(R, E) + 1;
-  const int n_ctiles = (int)ceil_div(No, S::BN);
-  const dim3 grid((unsigned)(8 * ceil_div(blocks * n_ctiles, 8)));
-  const auto* pa = reinterpret_cast<const unsigned char*>(a);
-  const auto* pw = reinterpret_cast<const unsigned char*>(w);
-  if (out_bf16)
-    hipLaunchKernelGGL((grouped_rows_kernel<S, WCOL, true>), grid, dim3(S::kThreads), 0, st, pa, pw,
-                       offsets, out, R, E, No, Kc, n_ctiles, (int)blocks);
-  else
-    hipLaunchKernelGGL((grouped_rows_kernel<S, WCOL, false>), grid, dim3(S::kThreads), 0, st, pa,
-                       pw, offsets, out, R, E, No, Kc, n_ctiles, (int)blocks);
+  const int64_t lim = (int64_t(1) << 31) - 8;
+  bool ok = E * (ceil_div(N, 128) + 7) * (ceil_div(K, 128) + 7) < lim;
+  for (int64_t width : {N, K})
+    with_rows_tile(R, E, width, [&](auto s) {
+      using S = decltype(s);
+      ok = ok && max_blocks(R, E, S::BM) * ceil_div(width, S::BN) < lim;
+    });
+  return ok;
 }
 
 hipError_t launch_grouped_rows(const void* a, const void* w, const int32_t* offsets, void* out,
                                int R, int E, int No, int Kc, bool w_across, bool out_bf16,
                                hipStream_t st) {
-  if (w_across)
-    launch_rows<TileSmall, true>(a, w, offsets, out, R, E, No, Kc, out_bf16, st);
-  else
-    launch_rows<TileSmall, false>(a, w, offsets, out, R, E, No, Kc, out_bf16, st);
+  with_rows_tile(R, E, No, [&](auto s) {
+    using S = decltype(s);
+    const int64_t blocks = max_blocks(R, E, S::BM);
+    const int n_ctiles = (int)ceil_div(No, S::BN);
+    const dim3 grid((unsigned)(8 * ceil_div(blocks * n_ctiles, 8)));
+    auto go = [&](auto across, auto bf16) {
+      hipLaunchKernelGGL((grouped_rows_kernel<S, decltype(across)::value, decltype(bf16)::value>),
+                         grid, dim3(S::kThreads), 0, st, reinterpret_cast<const unsigned char*>(a),
+                         reinterpret_cast<const unsigned char*>(w), offsets,
+                         reinterpret_cast<unsigned char*>(out), R, E, No, Kc, n_ctiles, (int)blocks);
+    };
+    using Y = std::true_type;
+    using N = std::false_type;
+    if (w_across)
+      out_bf16 ? go(Y{}, Y{}) : go(Y{}, N{});
+    else
+      out_bf16 ? go(N{}, Y{}) : go(N{}, N{});
+  });
   return hipGetLastError();
+}
+
+using TileDwSmall = TileShape<128, 128, 2, 2, 2, 2>;
+
+template <class S>
+static void launch_dw(const void* dy, const void* x, const int32_t* offsets, void* dw, int R, int E,
+                      int N, int K, bool out_bf16, hipStream_t st) {
+  const int n_mtiles = (int)ceil_div(N, S::BM), n_ctiles = (int)ceil_div(K, S::BN);
+  const dim3 grid((unsigned)(8 * E * ceil_div((int64_t)n_mtiles * n_ctiles, 8)));
+  const auto* pd = reinterpret_cast<const unsigned char*>(dy);
+  const auto* px = reinterpret_cast<const unsigned char*>(x);
+  auto* po = reinterpret_cast<unsigned char*>(dw);
+  if (out_bf16)
+    hipLaunchKernelGGL((grouped_dw_kernel<S, true>), grid, dim3(S::kThreads), 0, st, pd, px,
+                       offsets, po, R, E, N, K, n_mtiles, n_ctiles);
+  else
+    hipLaunchKernelGGL((grouped_dw_kernel<S, false>), grid, dim3(S::kThreads), 0, st, pd, px,
+                       offsets, po, R, E, N, K, n_mtiles, n_ctiles);
 }
 
 hipError_t launch_grouped_dw(const void* dy, const void* x, const int32_t* offsets, void* dw, int R,
                              int E, int N, int K, bool out_bf16, hipStream_t st) {
-  using S = TileSmall;
-  const int n_mtiles = (int)ceil_div(N, S::BM), n_ctiles = (int)ceil_div(K, S::BN);
-  const dim3 grid((unsigned)(8 * ceil_div((int64_t)E * n_mtiles * n_ctiles, 8)));
-  const auto* pd = reinterpret_cast<const unsigned char*>(dy);
-  const auto* px = reinterpret_cast<const unsigned char*>(x);
-  if (out_bf16)
-    hipLaunchKernelGGL((grouped_dw_kernel<S, true>), grid, dim3(S::kThreads), 0, st, pd, px,
-                       offsets, dw, R, E, N, K, n_mtiles, n_ctiles);
+  // 256 x 256 tiles where they fill the GPU (1.89 ms against 2.21 at the size above, bf16 gradients
+  // 1.64 against 1.88; with few rows both wait for the stores: 48 us for 201 MB)
+  if (E * ceil_div(N, 256) * ceil_div(K, 256) >= kGroupedCus)
+    launch_dw<Tile256>(dy, x, offsets, dw, R, E, N, K, out_bf16, st);
   else
-    hipLaunchKernelGGL((grouped_dw_kernel<S, false>), grid, dim3(S::kThreads), 0, st, pd, px,
-                       offsets, dw, R, E, N, K, n_mtiles, n_ctiles);
+    launch_dw<TileDwSmall>(dy, x, offsets, dw, R, E, N, K, out_bf16, st);
   return hipGetLastError();
 }
 

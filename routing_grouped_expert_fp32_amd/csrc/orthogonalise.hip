@@ -124,16 +124,13 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   const int row0 = i * S::BM, col0 = j * S::BN;
   const _Float16* xm = x + (int64_t)mat * m * ld;
   const int64_t ldb = (int64_t)ld * 2;
-  OperandLoader<S::BM, S::kWaves, false> la;
-  OperandLoader<S::BN, S::kWaves, false> lb;
+  OperandLoader<S::BM, S::kWaves, false, S::KT> la;
+  OperandLoader<S::BN, S::kWaves, false, S::KT> lb;
   const auto* xb = reinterpret_cast<const unsigned char*>(xm);
   la.init({xb + row0 * ldb, ldb, min(S::BM, m - row0), 0}, wave, lane);
   lb.init({xb + col0 * ldb, ldb, min(S::BN, m - col0), 0}, wave, lane);
   floatx4 acc[S::FM][S::FN];
-#pragma unroll
-  for (int p = 0; p < S::FM; ++p)
-#pragma unroll
-    for (int q = 0; q < S::FN; ++q) acc[p][q] = floatx4{0.f, 0.f, 0.f, 0.f};
+  tile_zero<S>(acc);
   tile_kloop<S, false, false, true, S::FM>(la, lb, k, smem, wave, lane, acc);
   _Float16* om = out + (int64_t)mat * m * mp;
   tile_for_each<S, S::FM>(acc, wave, lane, [&](int dm, int dn, floatx4 d) {
@@ -171,8 +168,8 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   const int mat = blockIdx.x / per, t = blockIdx.x % per;
   const int row0 = t % n_mtiles * S::BM, col0 = t / n_mtiles * S::BN;
   const int64_t x0 = (int64_t)mat * m * ld;
-  OperandLoader<S::BM, S::kWaves, false> la;
-  OperandLoader<S::BN, S::kWaves, true> lb;
+  OperandLoader<S::BM, S::kWaves, false, S::KT> la;
+  OperandLoader<S::BN, S::kWaves, true, S::KT> lb;
   la.init({reinterpret_cast<const unsigned char*>(bmat + (int64_t)mat * m * mp) +
                (int64_t)row0 * mp * 2,
            (int64_t)mp * 2, min(S::BM, m - row0), 0},
@@ -181,10 +178,7 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
            (ld - col0) * 2},
           wave, lane);
   floatx4 acc[S::FM][S::FN];
-#pragma unroll
-  for (int p = 0; p < S::FM; ++p)
-#pragma unroll
-    for (int q = 0; q < S::FN; ++q) acc[p][q] = floatx4{0.f, 0.f, 0.f, 0.f};
+  tile_zero<S>(acc);
   tile_kloop<S, false, true, true, S::FM>(la, lb, m, smem, wave, lane, acc);
   tile_for_each<S, S::FM>(acc, wave, lane, [&](int dm, int dn, floatx4 d) {
     const int r = row0 + dm, c = col0 + dn;
@@ -232,7 +226,7 @@ NsLayout ns_layout(int64_t n_mats, int rows, int cols) {
   return L;
 }
 
-using NsTile = TileShape<128, 128, 2, 2, 2>;
+using NsTile = TileShape<128, 128, 2, 2, 2, 2>;
 
 bool ns_grid_fits(int64_t n_mats, int rows, int cols) {
   const int64_t mt = ceil_div(std::min(rows, cols), 128), ct = ceil_div(std::max(rows, cols), 128);
