@@ -175,9 +175,10 @@ int boundary_bwd_parts(int64_t T);
 hipError_t launch_boundary_bwd(const BoundaryBwdArgs& a, int64_t T, int H, hipStream_t st);
 
 // Workspace of the orthogonalised update (byte offsets): partial sums of squares, X as hi (two, in
-// turn) + lo, A and B; m <= n its sides, mp and ld their padded row lengths.
+// turn) + lo, A and B, partial sums of A; m <= n its sides, mp and ld their padded row lengths.
 struct NsLayout {
-  size_t parts = 0, hi[2] = {0, 0}, lo = 0, gram = 0, poly = 0, total = 0;
+  size_t parts = 0, hi[2] = {0, 0}, lo = 0, gram = 0, poly = 0, sums = 0,
+         total = 0;
   int m = 0, n = 0, mp = 0, ld = 0;
   bool tall = false;
 };

@@ -96,32 +96,56 @@ __global__ __launch_bounds__(256) void ns_init_kernel(const void* __restrict__ g
   }
 }
 
-__device__ __forceinline__ f16x4 to_f16x4(floatx4 v) {
-  return f16x4{(_Float16)v.x, (_Float16)v.y, (_Float16)v.z, (_Float16)v.w};
+// Two values rounded to fp16, to nearest even.
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, (f16x2{(_Float16)a, (_Float16)b}));
 }
-__device__ __forceinline__ floatx4 from_f16x4(f16x4 v) {
-  return floatx4{(float)v.x, (float)v.y, (float)v.z, (float)v.w};
+__device__ __forceinline__ f16x8 load_f16x8(const _Float16* p) {
+  return *reinterpret_cast<const f16x8*>(p);
+}
+
+// Lane b of each four holds row b of a 4 x 4 matrix of 16-bit values (r0: columns 0, 1; r1: 2, 3);
+// afterwards it holds column b.
+__device__ __forceinline__ u32x2 quad_transpose(uint32_t r0, uint32_t r1, int lane) {
+  auto from = [](uint32_t v, auto ctrl) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, decltype(ctrl)::value, 0xf, 0xf, true);
+  };
+  using Xor1 = std::integral_constant<int, 0xB1>;   // quad_perm 1, 0, 3, 2
+  using Xor2 = std::integral_constant<int, 0x4E>;   // quad_perm 2, 3, 0, 1
+  const uint32_t sel = lane & 1 ? 0x03020706u : 0x05040100u;
+  const uint32_t s0 = __builtin_amdgcn_perm(from(r0, Xor1{}), r0, sel);
+  const uint32_t s1 = __builtin_amdgcn_perm(from(r1, Xor1{}), r1, sel);
+  const bool low = (lane & 2) == 0;
+  const uint32_t t = from(low ? s1 : s0, Xor2{});
+  return low ? u32x2{s0, t} : u32x2{t, s1};
+}
+
+// Row i, column j <= i of the lower triangle's tile t.
+__device__ __forceinline__ void triangle_tile(int t, int& i, int& j) {
+  i = (int)((sqrtf(8.f * t + 1.f) - 1.f) * 0.5f);
+  while (i * (i + 1) / 2 > t) --i;
+  while ((i + 1) * (i + 2) / 2 <= t) ++i;
+  j = t - i * (i + 1) / 2;
 }
 
 // D = X X^T of `x` [m][ld] (contraction over k values of each row): tiles on or under the diagonal,
-// written to both halves.
+// written to both halves of out [m][mp].
 //   POLY = false: out = D * c0                               (x = hi: A)
 //   POLY = true:  out = b x + D * c0 + ident on the diagonal (x = A:  B + s I)
+// The mirrored half goes out in 8-byte pieces after a 4 x 4 transpose between neighbouring lanes.
 template <class S, bool POLY>
 __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) void ns_gram_kernel(
     const _Float16* __restrict__ x, _Float16* __restrict__ out, int m, int mp, int ld, int k,
-    int n_tiles, int n_mats, float c0, float b, float ident) {
+    int per, float c0, float b, float ident) {
   static_assert(S::BM == S::BN, "square tiles");
   __shared__ __attribute__((aligned(16))) unsigned char smem[S::kLdsBytes];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int per = n_tiles * (n_tiles + 1) / 2;
-  const int mat = blockIdx.x / per, t = blockIdx.x % per;
-  int i = (int)((sqrtf(8.f * t + 1.f) - 1.f) * 0.5f);   // row i of the triangle holds t
-  while (i * (i + 1) / 2 > t) --i;
-  while ((i + 1) * (i + 2) / 2 <= t) ++i;
-  const int j = t - i * (i + 1) / 2;
-  const int row0 = i * S::BM, col0 = j * S::BN;
+  const int mat = blockIdx.x / per;
+  int ti, tj;
+  triangle_tile(blockIdx.x % per, ti, tj);
+  const int row0 = uniform(ti) * S::BM, col0 = uniform(tj) * S::BN;
   const _Float16* xm = x + (int64_t)mat * m * ld;
   const int64_t ldb = (int64_t)ld * 2;
   OperandLoader<S::BM, S::kWaves, false, S::KT> la;
@@ -135,32 +159,92 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   _Float16* om = out + (int64_t)mat * m * mp;
   tile_for_each<S, S::FM>(acc, wave, lane, [&](int dm, int dn, floatx4 d) {
     const int r = row0 + dm, c = col0 + dn;
-    if (r >= mp || c >= mp) return;
-    floatx4 v = d * c0;   // zero in rows and columns m .. mp - 1
-    if (POLY && r < m) {
-      v = v + b * from_f16x4(*reinterpret_cast<const f16x4*>(xm + (int64_t)r * ld + c));
+    floatx4 v = d * c0;   // zero in rows and columns from m on
+    if (POLY && r < m && c < mp) {
+      const f16x4 a = *reinterpret_cast<const f16x4*>(xm + (int64_t)r * ld + c);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (r == c + q) v[q] += ident;
+      for (int q = 0; q < 4; ++q) v[q] += b * (float)a[q] + (r == c + q ? ident : 0.f);
     }
-    const f16x4 h = to_f16x4(v);
-    if (r < m) *reinterpret_cast<f16x4*>(om + (int64_t)r * mp + c) = h;
-    if (i != j) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (c + q < m) om[(int64_t)(c + q) * mp + r] = h[q];
+    const u32x2 h{pack_f16(v.x, v.y), pack_f16(v.z, v.w)};
+    if (r < m && c < mp) *reinterpret_cast<u32x2*>(om + (int64_t)r * mp + c) = h;
+    if (row0 != col0) {
+      const u32x2 t = quad_transpose(h.x, h.y, lane);   // row c + lane % 4, columns r - r % 4 ..
+      const int mr = c + (lane & 3), mc = r - (lane & 3);
+      if (mr < m && mc < mp) *reinterpret_cast<u32x2*>(om + (int64_t)mr * mp + mc) = t;
     }
   });
 }
 
-// X' = a lo + (a - s) hi + (B + s I) hi, as hi' + lo', or, in the last step, rounded to bf16 into
-// `out` in G's own layout.
+// Part of A's sums for a matrix whose tiles leave most CUs idle: the contraction is cut into `parts`
+// of kp values, and part p of tile t goes to sums[(mat * per + t) * parts + p] (BM x BN fp32).
+template <class S>
+__global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) void ns_gram_part_kernel(
+    const _Float16* __restrict__ x, float* __restrict__ sums, int m, int ld, int k, int per,
+    int parts, int kp) {
+  __shared__ __attribute__((aligned(16))) unsigned char smem[S::kLdsBytes];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = blockIdx.x % parts, tile = blockIdx.x / parts % per;
+  const int mat = blockIdx.x / parts / per;
+  int ti, tj;
+  triangle_tile(tile, ti, tj);
+  const int row0 = uniform(ti) * S::BM, col0 = uniform(tj) * S::BN;
+  const int64_t ldb = (int64_t)ld * 2;
+  const auto* xb = reinterpret_cast<const unsigned char*>(x + (int64_t)mat * m * ld + part * kp);
+  OperandLoader<S::BM, S::kWaves, false, S::KT> la;
+  OperandLoader<S::BN, S::kWaves, false, S::KT> lb;
+  // (a part's last row may reach past the matrix by the offset of the part: its loads past k are
+  // kept out by k, not by the buffer's end)
+  la.init({xb + row0 * ldb, ldb, min(S::BM, m - row0), 0}, wave, lane);
+  lb.init({xb + col0 * ldb, ldb, min(S::BN, m - col0), 0}, wave, lane);
+  floatx4 acc[S::FM][S::FN];
+  tile_zero<S>(acc);
+  tile_kloop<S, false, false, true, S::FM>(la, lb, min(kp, k - part * kp), smem, wave, lane, acc);
+  float* o = sums + (int64_t)blockIdx.x * (S::BM * S::BN);
+  tile_for_each<S, S::FM>(acc, wave, lane, [&](int dm, int dn, floatx4 d) {
+    *reinterpret_cast<floatx4*>(o + dm * S::BN + dn) = d;
+  });
+}
+
+// A = c0 * the parts' sum, in part order, to both halves. A workgroup per quarter of a tile.
+template <class S>
+__global__ __launch_bounds__(256) void ns_gram_sum_kernel(const float* __restrict__ sums,
+                                                          _Float16* __restrict__ out, int m, int mp,
+                                                          int per, int parts, float c0) {
+  const int lane = threadIdx.x & 63;
+  const int tile = blockIdx.x / 4 % per, mat = blockIdx.x / 4 / per;
+  int ti, tj;
+  triangle_tile(tile, ti, tj);
+  constexpr int kQuads = S::BN / 4;   // runs of four columns of a row
+  static_assert(S::BM * kQuads == 4 * 256, "one run a thread");
+  // 16 rows by 4 runs a wave, as a sub-tile's accumulators lie
+  const int sub = blockIdx.x % 4 * 4 + (threadIdx.x >> 6);
+  const int dm = sub / (S::BN / 16) * 16 + (lane & 15);
+  const int dn = sub % (S::BN / 16) * 16 + 4 * (lane >> 4);
+  const float* p = sums + ((int64_t)mat * per + tile) * parts * (S::BM * S::BN) + dm * S::BN + dn;
+  floatx4 v = *reinterpret_cast<const floatx4*>(p);
+  for (int i = 1; i < parts; ++i)
+    v += *reinterpret_cast<const floatx4*>(p + (int64_t)i * (S::BM * S::BN));
+  v = v * c0;
+  _Float16* om = out + (int64_t)mat * m * mp;
+  const int r = ti * S::BM + dm, c = tj * S::BN + dn;
+  const u32x2 h{pack_f16(v.x, v.y), pack_f16(v.z, v.w)};
+  if (r < m && c < mp) *reinterpret_cast<u32x2*>(om + (int64_t)r * mp + c) = h;
+  if (ti != tj) {
+    const u32x2 t = quad_transpose(h.x, h.y, lane);
+    const int mr = c + (lane & 3), mc = r - (lane & 3);
+    if (mr < m && mc < mp) *reinterpret_cast<u32x2*>(om + (int64_t)mr * mp + mc) = t;
+  }
+}
+
+// X' = c_lo lo + c_hi hi + c_prod (B + s I) hi, as hi' + lo', or, in the last step, rounded to bf16
+// into `out` in G's own layout.
 template <class S, bool LAST>
 __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) void ns_update_kernel(
     const _Float16* __restrict__ bmat, const _Float16* __restrict__ hi, _Float16* lo,
     _Float16* __restrict__ hi_out, uint16_t* __restrict__ out, int m, int mp, int n, int ld,
-    int n_mtiles, int n_ctiles, int n_mats, float c_prod, float c_hi, float c_lo, float c_out,
-    int tall) {
+    int n_mtiles, int n_ctiles, float c_prod, float c_hi, float c_lo, float c_out, int tall) {
+  static_assert(S::FN % 2 == 0, "sub-tiles in pairs");
   __shared__ __attribute__((aligned(16))) unsigned char smem[S::kLdsBytes];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -180,26 +264,83 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   floatx4 acc[S::FM][S::FN];
   tile_zero<S>(acc);
   tile_kloop<S, false, true, true, S::FM>(la, lb, m, smem, wave, lane, acc);
-  tile_for_each<S, S::FM>(acc, wave, lane, [&](int dm, int dn, floatx4 d) {
-    const int r = row0 + dm, c = col0 + dn;
-    if (r >= m || c >= ld) return;
-    const int64_t at = x0 + (int64_t)r * ld + c;
-    const floatx4 h = from_f16x4(*reinterpret_cast<const f16x4*>(hi + at));
-    const floatx4 l = from_f16x4(*reinterpret_cast<const f16x4*>(lo + at));
-    const floatx4 v = c_prod * d + c_hi * h + c_lo * l;   // zero in columns n .. ld - 1
-    if constexpr (!LAST) {
-      const f16x4 nh = to_f16x4(v);
-      *reinterpret_cast<f16x4*>(hi_out + at) = nh;
-      *reinterpret_cast<f16x4*>(lo + at) = to_f16x4(v - from_f16x4(nh));
-    } else {
-      const int64_t o0 = (int64_t)mat * m * n;
+  // two neighbouring sub-tiles at a time: after a swap with the lane 16 away a lane has eight
+  // consecutive columns of one of them (lanes g = 0, 2: the first, g = 1, 3: the second)
+  const int g = lane >> 4;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (c + q < n)
-          out[o0 + (tall ? (int64_t)(c + q) * m + r : (int64_t)r * n + c + q)] =
-              (uint16_t)f32_to_bf16_bits(c_out * v[q]);
+  for (int i = 0; i < S::FM; ++i) {
+    const int r = row0 + 16 * (wave / S::WN + S::WM * i) + (lane & 15);
+#pragma unroll
+    for (int j = 0; j < S::FN; j += 2) {
+      const int c = col0 + 16 * (wave % S::WN * S::FN + j + (g & 1)) + 4 * (g & 2);
+      float d[8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const auto sw = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][j][q]),
+                                                         __float_as_uint(acc[i][j + 1][q]), false,
+                                                         false);
+        d[q] = __uint_as_float(sw[0]);
+        d[q + 4] = __uint_as_float(sw[1]);
+      }
+      if (r >= m || c >= ld) continue;   // ld % 8 == 0: eight columns are all in or all out
+      const int64_t at = x0 + (int64_t)r * ld + c;
+      const f16x8 h = load_f16x8(hi + at), l = load_f16x8(lo + at);
+      // zero in columns n .. ld - 1
+#pragma unroll
+      for (int q = 0; q < 8; ++q) d[q] = c_prod * d[q] + c_hi * (float)h[q] + c_lo * (float)l[q];
+      if constexpr (!LAST) {
+        f16x8 nh, nl;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          nh[q] = (_Float16)d[q];
+          nl[q] = (_Float16)(d[q] - (float)nh[q]);
+        }
+        *reinterpret_cast<f16x8*>(hi_out + at) = nh;
+        *reinterpret_cast<f16x8*>(lo + at) = nl;
+      } else {
+        uint16_t* o = out + (int64_t)mat * m * n;
+        if (!tall && (n & 7) == 0) {
+          u32x4 w;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) w[q] = pack_bf16(c_out * d[2 * q], c_out * d[2 * q + 1]);
+          *reinterpret_cast<u32x4*>(o + (int64_t)r * n + c) = w;
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (c + q < n)
+              o[tall ? (int64_t)(c + q) * m + r : (int64_t)r * n + c + q] =
+                  (uint16_t)pack_bf16(c_out * d[q], 0.f);
+        }
+      }
     }
-  });
+  }
+}
+
+// ---- host side -----------------------------------------------------------------------------------
+using NsTile256 = TileShape<256, 256, 2, 4, 2, 2>;
+using NsTile128 = TileShape<128, 128, 2, 2, 2, 2>;
+using NsTile64 = TileShape<64, 64, 1, 2, 3, 3>;
+constexpr int kNsCus = 256;
+
+static int64_t triangle(int64_t n) { return n * (n + 1) / 2; }
+
+// The largest tile whose workgroups fill the GPU; `count` is their number for a tile side.
+template <class Count, class F>
+static void with_ns_tile(Count&& count, F&& f) {
+  if (count(256) >= kNsCus)
+    f(NsTile256{});
+  else if (count(128) >= kNsCus)
+    f(NsTile128{});
+  else
+    f(NsTile64{});
+}
+
+// Parts of the contraction of A's products: one unless 64 x 64 tiles do not fill the GPU; then up to
+// two workgroups a CU, of at least four stages each.
+static int gram_parts(int64_t n_mats, int m, int k) {
+  const int64_t tiles = n_mats * triangle(ceil_div(m, 64));
+  if (tiles >= kNsCus) return 1;
+  return (int)std::max<int64_t>(1, std::min(2 * kNsCus / tiles, ceil_div(k, 256)));
 }
 
 NsLayout ns_layout(int64_t n_mats, int rows, int cols) {
@@ -222,14 +363,15 @@ NsLayout ns_layout(int64_t n_mats, int rows, int cols) {
   L.lo = take(x);
   L.gram = take(a);
   L.poly = take(a);
+  const int np = gram_parts(n_mats, L.m, L.n);
+  if (np > 1)
+    L.sums = take(sizeof(float) * 64 * 64 * (size_t)(np * n_mats * triangle(ceil_div(L.m, 64))));
   L.total = off;
   return L;
 }
 
-using NsTile = TileShape<128, 128, 2, 2, 2, 2>;
-
 bool ns_grid_fits(int64_t n_mats, int rows, int cols) {
-  const int64_t mt = ceil_div(std::min(rows, cols), 128), ct = ceil_div(std::max(rows, cols), 128);
+  const int64_t mt = ceil_div(std::min(rows, cols), 64), ct = ceil_div(std::max(rows, cols), 64);
   return n_mats <= 65535 && n_mats * mt * std::max(ct, (mt + 1) / 2) < (int64_t(1) << 31);
 }
 
@@ -237,7 +379,7 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
                                 int cols, int steps, const float* coeffs, float eps, char* ws,
                                 hipStream_t st) {
   const NsLayout L = ns_layout(n_mats, rows, cols);
-  double* parts = reinterpret_cast<double*>(ws + L.parts);
+  double* norm_parts = reinterpret_cast<double*>(ws + L.parts);
   _Float16* hi[2] = {reinterpret_cast<_Float16*>(ws + L.hi[0]),
                      reinterpret_cast<_Float16*>(ws + L.hi[1])};
   _Float16* lo = reinterpret_cast<_Float16*>(ws + L.lo);
@@ -247,29 +389,59 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
   const float sx = x_scale(L.n);
   const float ident = std::round(-(b + c) * 4.f) / 4.f;   // exact in fp16 at the stored scale
   hipLaunchKernelGGL(ns_norm_kernel, dim3(kNormParts, n_mats), dim3(256), 0, st, g, g_bf16,
-                     (int64_t)rows * cols, parts);
+                     (int64_t)rows * cols, norm_parts);
   hipLaunchKernelGGL(ns_init_kernel,
                      dim3((unsigned)ceil_div(L.ld, 64), (unsigned)ceil_div(L.m, 64), n_mats),
-                     dim3(256), 0, st, g, g_bf16, rows, cols, L.tall, L.m, L.ld, parts, sx, eps,
+                     dim3(256), 0, st, g, g_bf16, rows, cols, L.tall, L.m, L.ld, norm_parts, sx, eps,
                      hi[0], lo);
-  using S = NsTile;
-  const int mt = (int)ceil_div(L.m, S::BM), ct = (int)ceil_div(L.ld, S::BN);
-  const dim3 gram_grid((unsigned)((int64_t)n_mats * mt * (mt + 1) / 2));
-  const dim3 upd_grid((unsigned)((int64_t)n_mats * mt * ct));
+  const int parts = gram_parts(n_mats, L.m, L.n);
+  auto gram_tiles = [&](int side) { return n_mats * triangle(ceil_div(L.m, side)); };
   for (int s = 0; s < steps; ++s) {
-    hipLaunchKernelGGL((ns_gram_kernel<S, false>), gram_grid, dim3(S::kThreads), 0, st, hi[0], gram,
-                       L.m, L.mp, L.ld, L.n, mt, n_mats, kGramScale / (sx * sx), 0.f, 0.f);
-    hipLaunchKernelGGL((ns_gram_kernel<S, true>), gram_grid, dim3(S::kThreads), 0, st, gram, poly,
-                       L.m, L.mp, L.mp, L.m, mt, n_mats, c / kGramScale, b, ident * kGramScale);
-    auto update = [&](auto last) {
-      hipLaunchKernelGGL((ns_update_kernel<S, decltype(last)::value>), upd_grid, dim3(S::kThreads),
-                         0, st, poly, hi[0], lo, hi[1], out, L.m, L.mp, L.n, L.ld, mt, ct, n_mats,
-                         1.f / kGramScale, a - ident, a, 1.f / sx, L.tall);
-    };
-    if (s + 1 == steps)
-      update(std::true_type{});
-    else
-      update(std::false_type{});
+    const float c0 = kGramScale / (sx * sx);
+    if (parts > 1) {
+      using S = NsTile64;
+      float* sums = reinterpret_cast<float*>(ws + L.sums);
+      const int per = (int)triangle(ceil_div(L.m, 64));
+      const int kp = (int)ceil_div(ceil_div(L.n, parts), 64) * 64;
+      const int used = (int)ceil_div(L.n, kp);   // rounding to stages can leave fewer parts
+      hipLaunchKernelGGL((ns_gram_part_kernel<S>), dim3((unsigned)(n_mats * per * used)),
+                         dim3(S::kThreads), 0, st, hi[0], sums, L.m, L.ld, L.n, per, used, kp);
+      hipLaunchKernelGGL((ns_gram_sum_kernel<S>), dim3((unsigned)(n_mats * per * 4)), dim3(256), 0,
+                         st, sums, gram, L.m, L.mp, per, used, c0);
+    } else {
+      with_ns_tile(gram_tiles, [&](auto tile) {
+        using S = decltype(tile);
+        hipLaunchKernelGGL((ns_gram_kernel<S, false>), dim3((unsigned)gram_tiles(S::BM)),
+                           dim3(S::kThreads), 0, st, hi[0], gram, L.m, L.mp, L.ld, L.n,
+                           (int)triangle(ceil_div(L.m, S::BM)), c0, 0.f, 0.f);
+      });
+    }
+    with_ns_tile(gram_tiles, [&](auto tile) {
+      using S = decltype(tile);
+      hipLaunchKernelGGL((ns_gram_kernel<S, true>), dim3((unsigned)gram_tiles(S::BM)),
+                         dim3(S::kThreads), 0, st, gram, poly, L.m, L.mp, L.mp, L.m,
+                         (int)triangle(ceil_div(L.m, S::BM)), c / kGramScale, b,
+                         ident * kGramScale);
+    });
+    auto update_tiles = [&](int side) { return n_mats * ceil_div(L.m, side) * ceil_div(L.ld, side); };
+    with_ns_tile(update_tiles, [&](auto tile) {
+      using S = decltype(tile);
+      const int mt = (int)ceil_div(L.m, S::BM), ct = (int)ceil_div(L.ld, S::BN);
+      auto update = [&](auto last) {
+        // lo takes a in every step but the last, a - s there: the error is B lo, which vanishes in
+        // weak directions, or (B + s I) lo, which vanishes in converged ones; only the last step's
+        // error is not amplified in the weak ones
+        constexpr bool kLast = decltype(last)::value;
+        hipLaunchKernelGGL((ns_update_kernel<S, kLast>), dim3((unsigned)update_tiles(S::BM)),
+                           dim3(S::kThreads), 0, st, poly, hi[0], lo, hi[1], out, L.m, L.mp, L.n,
+                           L.ld, mt, ct, 1.f / kGramScale, a - ident, kLast ? a - ident : a,
+                           1.f / sx, L.tall);
+      };
+      if (s + 1 == steps)
+        update(std::true_type{});
+      else
+        update(std::false_type{});
+    });
     std::swap(hi[0], hi[1]);
   }
   return hipGetLastError();
