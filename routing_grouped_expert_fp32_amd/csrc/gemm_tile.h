@@ -315,6 +315,13 @@ __device__ __forceinline__ void tile_for_each(const floatx4 (&acc)[S::FM][S::FN]
         16 * (wave % S::WN * S::FN + j) + 4 * (lane >> 4), acc[i][j]);
 }
 
+// Tile v of `total` for workgroup `wg` of a grid of 8 ceil(total / 8), one run of tiles per XCD.
+__device__ __forceinline__ int xcd_tile(int wg, int total) {
+  const int per = (total + 7) >> 3, local = wg >> 3;
+  const int v = (wg & 7) * per + local;
+  return local < per && v < total ? v : -1;
+}
+
 // Two values rounded to bf16, to nearest even, by one conversion instruction.
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   typedef float f32x2 __attribute__((ext_vector_type(2)));

@@ -97,13 +97,6 @@ struct BlockScan {
   }
 };
 
-// Tile v of `total` for workgroup `wg` of a grid of 8 ceil(total / 8), one run of tiles per XCD.
-__device__ __forceinline__ int xcd_tile(int wg, int total) {
-  const int per = (total + 7) >> 3, local = wg >> 3;
-  const int v = (wg & 7) * per + local;
-  return local < per && v < total ? v : -1;
-}
-
 constexpr int kTileGroup = 4;   // blocks of one expert walked together, column tile by column tile
 
 // out[row][0 .. No) = a[row][0 .. Kc) . w[e], w stored [No][Kc] (forward) or, WCOL, [Kc][No] (input

@@ -20,7 +20,7 @@
 
 namespace beam {
 
-constexpr int kNormParts = 64;          // partial sums of squares of a matrix
+constexpr int kNormParts = 512;         // partial sums of squares of a matrix
 constexpr float kGramScale = 256.f;     // A and B hold 2^8 times their values
 
 // X holds 2^k times its values, 2^k about sqrt(longer side): a matrix of orthonormal rows has entries
@@ -36,16 +36,46 @@ __device__ __forceinline__ float load_as_f32(const void* p, int64_t i, bool bf16
               : reinterpret_cast<const float*>(p)[i];
 }
 
-// Partial sums of squares, in 64 bits so that no finite input overflows or vanishes.
+// Eight consecutive values, the first at a multiple of 8.
+__device__ __forceinline__ void load8(const void* p, int64_t i, bool bf16, float* v) {
+  if (bf16) {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(p) + i);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[2 * q] = bf16_lo(w[q]);
+      v[2 * q + 1] = bf16_hi(w[q]);
+    }
+  } else {
+    const auto* f = reinterpret_cast<const floatx4*>(reinterpret_cast<const float*>(p) + i);
+    const floatx4 a = f[0], b = f[1];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[q] = a[q];
+      v[q + 4] = b[q];
+    }
+  }
+}
+
+// Partial sums of squares, in 64 bits so that no finite input overflows or vanishes. Matrices of a
+// multiple of 8 values are read 16 bytes (fp32: 32) at a time.
 __global__ __launch_bounds__(256) void ns_norm_kernel(const void* __restrict__ g, int g_bf16,
                                                       int64_t count, double* __restrict__ parts) {
   __shared__ double red[4];
   const int64_t base = (int64_t)blockIdx.y * count;
+  const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
   double s = 0.0;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count;
-       i += (int64_t)gridDim.x * 256) {
-    const double v = load_as_f32(g, base + i, g_bf16);
-    s += v * v;
+  if ((count & 7) == 0) {
+    for (int64_t i = first; i < count / 8; i += step) {
+      float v[8];
+      load8(g, base + 8 * i, g_bf16, v);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s += (double)v[q] * v[q];
+    }
+  } else {
+    for (int64_t i = first; i < count; i += step) {
+      const double v = load_as_f32(g, base + i, g_bf16);
+      s += v * v;
+    }
   }
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
@@ -64,34 +94,59 @@ __global__ __launch_bounds__(256) void ns_init_kernel(const void* __restrict__ g
                                                       _Float16* __restrict__ hi,
                                                       _Float16* __restrict__ lo) {
   __shared__ float tile[64][65];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
   const int64_t mat = blockIdx.z;
-  double s = parts[mat * kNormParts + lane];
+  double s = 0.0;
+#pragma unroll
+  for (int p = 0; p < kNormParts / 64; ++p) s += parts[mat * kNormParts + 64 * p + lane];
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
   const double den = sqrt(s) + (double)eps;
   const double mul = den > 0.0 ? (double)scale / den : 0.0;   // a zero matrix stays zero
   const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;   // tile origin in X
-  for (int i = wave; i < 64; i += 4) {
-    // X(r, c) = G(r, c), or G(c, r) when tall: `lane` runs along G's rows either way
-    const int gr = tall ? c0 + i : r0 + i, gc = (tall ? r0 : c0) + lane;
-    float v = 0.f;
-    if (gr < rows && gc < cols)
-      v = (float)(load_as_f32(g, mat * rows * cols + (int64_t)gr * cols + gc, g_bf16) * mul);
-    if (tall)
-      tile[lane][i] = v;
-    else
-      tile[i][lane] = v;
+  // X(r, c) = G(r, c), or G(c, r) when tall; the tile's rows of G are gr0.., its columns gc0..
+  const int gr0 = tall ? c0 : r0, gc0 = tall ? r0 : c0;
+  const bool by8 = (cols & 7) == 0;   // then rows start at multiples of 8 values
+#pragma unroll
+  for (int it = 0; it < 2; ++it) {   // a thread reads eight values of one row of G
+    const int i = it * 32 + (threadIdx.x >> 3), c8 = 8 * (threadIdx.x & 7);
+    const int gr = gr0 + i, gc = gc0 + c8;
+    float v[8] = {};
+    if (gr < rows && gc < cols) {
+      const int64_t at = mat * rows * cols + (int64_t)gr * cols + gc;
+      if (by8) {
+        load8(g, at, g_bf16, v);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (gc + q < cols) v[q] = load_as_f32(g, at + q, g_bf16);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float x = (float)(v[q] * mul);
+      if (tall)
+        tile[c8 + q][i] = x;
+      else
+        tile[i][c8 + q] = x;
+    }
   }
   __syncthreads();
-  for (int i = wave; i < 64; i += 4) {
-    const int r = r0 + i, c = c0 + lane;
-    if (r < m && c < ld) {
-      const float v = tile[i][lane];   // columns n .. ld - 1 lie outside G: zero
-      const _Float16 h = (_Float16)v;
+#pragma unroll
+  for (int it = 0; it < 2; ++it) {
+    const int i = it * 32 + (threadIdx.x >> 3), c8 = 8 * (threadIdx.x & 7);
+    const int r = r0 + i, c = c0 + c8;
+    if (r < m && c < ld) {   // ld % 8 == 0; columns n .. ld - 1 lie outside G: zero
+      f16x8 h, l;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float x = tile[i][c8 + q];
+        h[q] = (_Float16)x;
+        l[q] = (_Float16)(x - (float)h[q]);
+      }
       const int64_t at = (mat * m + r) * ld + c;
-      hi[at] = h;
-      lo[at] = (_Float16)(v - (float)h);
+      *reinterpret_cast<f16x8*>(hi + at) = h;
+      *reinterpret_cast<f16x8*>(lo + at) = l;
     }
   }
 }
@@ -137,14 +192,16 @@ __device__ __forceinline__ void triangle_tile(int t, int& i, int& j) {
 template <class S, bool POLY>
 __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) void ns_gram_kernel(
     const _Float16* __restrict__ x, _Float16* __restrict__ out, int m, int mp, int ld, int k,
-    int per, float c0, float b, float ident) {
+    int per, int total, float c0, float b, float ident) {
   static_assert(S::BM == S::BN, "square tiles");
   __shared__ __attribute__((aligned(16))) unsigned char smem[S::kLdsBytes];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int mat = blockIdx.x / per;
+  const int v = xcd_tile(blockIdx.x, total);
+  if (v < 0) return;
+  const int mat = v / per;
   int ti, tj;
-  triangle_tile(blockIdx.x % per, ti, tj);
+  triangle_tile(v % per, ti, tj);
   const int row0 = uniform(ti) * S::BM, col0 = uniform(tj) * S::BN;
   const _Float16* xm = x + (int64_t)mat * m * ld;
   const int64_t ldb = (int64_t)ld * 2;
@@ -223,6 +280,7 @@ __global__ __launch_bounds__(256) void ns_gram_sum_kernel(const float* __restric
   const int dn = sub % (S::BN / 16) * 16 + 4 * (lane >> 4);
   const float* p = sums + ((int64_t)mat * per + tile) * parts * (S::BM * S::BN) + dm * S::BN + dn;
   floatx4 v = *reinterpret_cast<const floatx4*>(p);
+#pragma unroll 8
   for (int i = 1; i < parts; ++i)
     v += *reinterpret_cast<const floatx4*>(p + (int64_t)i * (S::BM * S::BN));
   v = v * c0;
@@ -243,13 +301,15 @@ template <class S, bool LAST>
 __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) void ns_update_kernel(
     const _Float16* __restrict__ bmat, const _Float16* __restrict__ hi, _Float16* lo,
     _Float16* __restrict__ hi_out, uint16_t* __restrict__ out, int m, int mp, int n, int ld,
-    int n_mtiles, int n_ctiles, float c_prod, float c_hi, float c_lo, float c_out, int tall) {
+    int n_mtiles, int n_ctiles, int total, float c_prod, float c_hi, float c_lo, float c_out, int tall) {
   static_assert(S::FN % 2 == 0, "sub-tiles in pairs");
   __shared__ __attribute__((aligned(16))) unsigned char smem[S::kLdsBytes];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int per = n_mtiles * n_ctiles;
-  const int mat = blockIdx.x / per, t = blockIdx.x % per;
+  const int v = xcd_tile(blockIdx.x, total);
+  if (v < 0) return;
+  const int mat = v / per, t = v % per;
   const int row0 = t % n_mtiles * S::BM, col0 = t / n_mtiles * S::BN;
   const int64_t x0 = (int64_t)mat * m * ld;
   OperandLoader<S::BM, S::kWaves, false, S::KT> la;
@@ -322,6 +382,7 @@ using NsTile128 = TileShape<128, 128, 2, 2, 2, 2>;
 using NsTile64 = TileShape<64, 64, 1, 2, 3, 3>;
 constexpr int kNsCus = 256;
 
+static dim3 xcd_grid(int64_t tiles) { return dim3((unsigned)(8 * ceil_div(tiles, 8))); }
 static int64_t triangle(int64_t n) { return n * (n + 1) / 2; }
 
 // The largest tile whose workgroups fill the GPU; `count` is their number for a tile side.
@@ -372,7 +433,7 @@ NsLayout ns_layout(int64_t n_mats, int rows, int cols) {
 
 bool ns_grid_fits(int64_t n_mats, int rows, int cols) {
   const int64_t mt = ceil_div(std::min(rows, cols), 64), ct = ceil_div(std::max(rows, cols), 64);
-  return n_mats <= 65535 && n_mats * mt * std::max(ct, (mt + 1) / 2) < (int64_t(1) << 31);
+  return n_mats <= 65535 && n_mats * mt * std::max(ct, (mt + 1) / 2) < (int64_t(1) << 31) - 8;
 }
 
 hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n_mats, int rows,
@@ -411,16 +472,17 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
     } else {
       with_ns_tile(gram_tiles, [&](auto tile) {
         using S = decltype(tile);
-        hipLaunchKernelGGL((ns_gram_kernel<S, false>), dim3((unsigned)gram_tiles(S::BM)),
+        hipLaunchKernelGGL((ns_gram_kernel<S, false>), xcd_grid(gram_tiles(S::BM)),
                            dim3(S::kThreads), 0, st, hi[0], gram, L.m, L.mp, L.ld, L.n,
-                           (int)triangle(ceil_div(L.m, S::BM)), c0, 0.f, 0.f);
+                           (int)triangle(ceil_div(L.m, S::BM)), (int)gram_tiles(S::BM), c0, 0.f,
+                           0.f);
       });
     }
     with_ns_tile(gram_tiles, [&](auto tile) {
       using S = decltype(tile);
-      hipLaunchKernelGGL((ns_gram_kernel<S, true>), dim3((unsigned)gram_tiles(S::BM)),
+      hipLaunchKernelGGL((ns_gram_kernel<S, true>), xcd_grid(gram_tiles(S::BM)),
                          dim3(S::kThreads), 0, st, gram, poly, L.m, L.mp, L.mp, L.m,
-                         (int)triangle(ceil_div(L.m, S::BM)), c / kGramScale, b,
+                         (int)triangle(ceil_div(L.m, S::BM)), (int)gram_tiles(S::BM), c / kGramScale, b,
                          ident * kGramScale);
     });
     auto update_tiles = [&](int side) { return n_mats * ceil_div(L.m, side) * ceil_div(L.ld, side); };
@@ -432,9 +494,9 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
         // weak directions, or (B + s I) lo, which vanishes in converged ones; only the last step's
         // error is not amplified in the weak ones
         constexpr bool kLast = decltype(last)::value;
-        hipLaunchKernelGGL((ns_update_kernel<S, kLast>), dim3((unsigned)update_tiles(S::BM)),
+        hipLaunchKernelGGL((ns_update_kernel<S, kLast>), xcd_grid(update_tiles(S::BM)),
                            dim3(S::kThreads), 0, st, poly, hi[0], lo, hi[1], out, L.m, L.mp, L.n,
-                           L.ld, mt, ct, 1.f / kGramScale, a - ident, kLast ? a - ident : a,
+                           L.ld, mt, ct, (int)update_tiles(S::BM), 1.f / kGramScale, a - ident, kLast ? a - ident : a,
                            1.f / sx, L.tall);
       };
       if (s + 1 == steps)
