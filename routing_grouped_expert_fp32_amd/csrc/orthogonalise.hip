@@ -214,22 +214,49 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   tile_zero<S>(acc);
   tile_kloop<S, false, false, true, S::FM>(la, lb, k, smem, wave, lane, acc);
   _Float16* om = out + (int64_t)mat * m * mp;
-  tile_for_each<S, S::FM>(acc, wave, lane, [&](int dm, int dn, floatx4 d) {
-    const int r = row0 + dm, c = col0 + dn;
-    floatx4 v = d * c0;   // zero in rows and columns from m on
-    if (POLY && r < m && c < mp) {
-      const f16x4 a = *reinterpret_cast<const f16x4*>(xm + (int64_t)r * ld + c);
+  // A's values of half the row sub-tiles are read together, ahead of their use: one at a time, their
+  // latencies took as long as the products
+  const int g = lane >> 4;
+  const int dn0 = col0 + 16 * (wave % S::WN * S::FN) + 4 * g;
+  constexpr int kBatch = S::FM / 2;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] += b * (float)a[q] + (r == c + q ? ident : 0.f);
+  for (int i0 = 0; i0 < S::FM; i0 += kBatch) {
+    f16x4 a[kBatch][S::FN];
+    if constexpr (POLY) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j) {
+          const int r = row0 + 16 * (wave / S::WN + S::WM * (i0 + i)) + (lane & 15);
+          const int c = dn0 + 16 * j;
+          // outside the matrix any value inside it does: its result is not stored
+          a[i][j] = *reinterpret_cast<const f16x4*>(xm + (int64_t)min(r, m - 1) * ld +
+                                                    min(c, mp - 4));
+        }
     }
-    const u32x2 h{pack_f16(v.x, v.y), pack_f16(v.z, v.w)};
-    if (r < m && c < mp) *reinterpret_cast<u32x2*>(om + (int64_t)r * mp + c) = h;
-    if (row0 != col0) {
-      const u32x2 t = quad_transpose(h.x, h.y, lane);   // row c + lane % 4, columns r - r % 4 ..
-      const int mr = c + (lane & 3), mc = r - (lane & 3);
-      if (mr < m && mc < mp) *reinterpret_cast<u32x2*>(om + (int64_t)mr * mp + mc) = t;
-    }
-  });
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j) {
+        const int r = row0 + 16 * (wave / S::WN + S::WM * (i0 + i)) + (lane & 15);
+        const int c = dn0 + 16 * j;
+        floatx4 v = acc[i0 + i][j] * c0;   // zero in rows and columns from m on
+        if constexpr (POLY) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            v[q] += b * (float)a[i][j][q] + (r == c + q ? ident : 0.f);
+            if (r >= m || c + q >= m) v[q] = 0.f;
+          }
+        }
+        const u32x2 h{pack_f16(v.x, v.y), pack_f16(v.z, v.w)};
+        if (r < m && c < mp) *reinterpret_cast<u32x2*>(om + (int64_t)r * mp + c) = h;
+        if (row0 != col0) {
+          const u32x2 t = quad_transpose(h.x, h.y, lane);   // row c + lane % 4, columns r - r % 4 ..
+          const int mr = c + (lane & 3), mc = r - (lane & 3);
+          if (mr < m && mc < mp) *reinterpret_cast<u32x2*>(om + (int64_t)mr * mp + mc) = t;
+        }
+      }
+  }
 }
 
 // Part of A's sums for a matrix whose tiles leave most CUs idle: the contraction is cut into `parts`
@@ -327,52 +354,67 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   // two neighbouring sub-tiles at a time: after a swap with the lane 16 away a lane has eight
   // consecutive columns of one of them (lanes g = 0, 2: the first, g = 1, 3: the second)
   const int g = lane >> 4;
+  const int c0 = col0 + 16 * (wave % S::WN * S::FN + (g & 1)) + 4 * (g & 2);
+  constexpr int kBatch = S::FM / 4;   // row sub-tiles whose hi and lo are read together
 #pragma unroll
-  for (int i = 0; i < S::FM; ++i) {
-    const int r = row0 + 16 * (wave / S::WN + S::WM * i) + (lane & 15);
+  for (int i0 = 0; i0 < S::FM; i0 += kBatch) {
+    f16x8 h[kBatch][S::FN / 2], l[kBatch][S::FN / 2];
 #pragma unroll
-    for (int j = 0; j < S::FN; j += 2) {
-      const int c = col0 + 16 * (wave % S::WN * S::FN + j + (g & 1)) + 4 * (g & 2);
-      float d[8];
+    for (int i = 0; i < kBatch; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const auto sw = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][j][q]),
-                                                         __float_as_uint(acc[i][j + 1][q]), false,
-                                                         false);
-        d[q] = __uint_as_float(sw[0]);
-        d[q + 4] = __uint_as_float(sw[1]);
+      for (int j = 0; j < S::FN / 2; ++j) {
+        const int r = row0 + 16 * (wave / S::WN + S::WM * (i0 + i)) + (lane & 15);
+        // outside the matrix any value inside it does: its result is not stored
+        const int64_t at = x0 + (int64_t)min(r, m - 1) * ld + min(c0 + 32 * j, ld - 8);
+        h[i][j] = load_f16x8(hi + at);
+        l[i][j] = load_f16x8(lo + at);
       }
-      if (r >= m || c >= ld) continue;   // ld % 8 == 0: eight columns are all in or all out
-      const int64_t at = x0 + (int64_t)r * ld + c;
-      const f16x8 h = load_f16x8(hi + at), l = load_f16x8(lo + at);
-      // zero in columns n .. ld - 1
 #pragma unroll
-      for (int q = 0; q < 8; ++q) d[q] = c_prod * d[q] + c_hi * (float)h[q] + c_lo * (float)l[q];
-      if constexpr (!LAST) {
-        f16x8 nh, nl;
+    for (int i = 0; i < kBatch; ++i)
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          nh[q] = (_Float16)d[q];
-          nl[q] = (_Float16)(d[q] - (float)nh[q]);
+      for (int j = 0; j < S::FN / 2; ++j) {
+        const int r = row0 + 16 * (wave / S::WN + S::WM * (i0 + i)) + (lane & 15);
+        const int c = c0 + 32 * j;
+        float d[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const auto sw = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i0 + i][2 * j][q]),
+                                                           __float_as_uint(acc[i0 + i][2 * j + 1][q]),
+                                                           false, false);
+          d[q] = __uint_as_float(sw[0]);
+          d[q + 4] = __uint_as_float(sw[1]);
         }
-        *reinterpret_cast<f16x8*>(hi_out + at) = nh;
-        *reinterpret_cast<f16x8*>(lo + at) = nl;
-      } else {
-        uint16_t* o = out + (int64_t)mat * m * n;
-        if (!tall && (n & 7) == 0) {
-          u32x4 w;
+        if (r >= m || c >= ld) continue;   // ld % 8 == 0: eight columns are all in or all out
+        const int64_t at = x0 + (int64_t)r * ld + c;
+        // zero in columns n .. ld - 1
 #pragma unroll
-          for (int q = 0; q < 4; ++q) w[q] = pack_bf16(c_out * d[2 * q], c_out * d[2 * q + 1]);
-          *reinterpret_cast<u32x4*>(o + (int64_t)r * n + c) = w;
+        for (int q = 0; q < 8; ++q)
+          d[q] = c_prod * d[q] + c_hi * (float)h[i][j][q] + c_lo * (float)l[i][j][q];
+        if constexpr (!LAST) {
+          f16x8 nh, nl;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            nh[q] = (_Float16)d[q];
+            nl[q] = (_Float16)(d[q] - (float)nh[q]);
+          }
+          *reinterpret_cast<f16x8*>(hi_out + at) = nh;
+          *reinterpret_cast<f16x8*>(lo + at) = nl;
         } else {
+          uint16_t* o = out + (int64_t)mat * m * n;
+          if (!tall && (n & 7) == 0) {
+            u32x4 w;
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (c + q < n)
-              o[tall ? (int64_t)(c + q) * m + r : (int64_t)r * n + c + q] =
-                  (uint16_t)pack_bf16(c_out * d[q], 0.f);
+            for (int q = 0; q < 4; ++q) w[q] = pack_bf16(c_out * d[2 * q], c_out * d[2 * q + 1]);
+            *reinterpret_cast<u32x4*>(o + (int64_t)r * n + c) = w;
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (c + q < n)
+                o[tall ? (int64_t)(c + q) * m + r : (int64_t)r * n + c + q] =
+                    (uint16_t)pack_bf16(c_out * d[q], 0.f);
+          }
         }
       }
-    }
   }
 }
 
@@ -385,10 +427,13 @@ constexpr int kNsCus = 256;
 static dim3 xcd_grid(int64_t tiles) { return dim3((unsigned)(8 * ceil_div(tiles, 8))); }
 static int64_t triangle(int64_t n) { return n * (n + 1) / 2; }
 
-// The largest tile whose workgroups fill the GPU; `count` is their number for a tile side.
+// The largest tile whose workgroups fill the GPU (256 x 256 ones from three quarters on: they multiply
+// a quarter faster); `count` is their number for a tile side. 2560 x 5120, us, 256 / 128 wide tiles:
+// A of 1, 2, 4, 8 matrices 123 / 58, 120 / 81, 134 / 153, 268 / 301; the update of 1, 8: 83 / 94,
+// 628 / 709.
 template <class Count, class F>
 static void with_ns_tile(Count&& count, F&& f) {
-  if (count(256) >= kNsCus)
+  if (count(256) >= kNsCus * 3 / 4)
     f(NsTile256{});
   else if (count(128) >= kNsCus)
     f(NsTile128{});
