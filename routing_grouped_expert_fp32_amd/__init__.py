@@ -366,27 +366,39 @@ def fp8_dot_tiles(a, b, c, stream=None):
     return d
 
 
-@contextlib.contextmanager
-def _placed(stream, *ts):
-    """Checks that the tensors (None skipped) are contiguous on one device, and makes that device and
-    the stream (default: its current one) current, so that results and workspaces allocated inside
-    belong to the stream that uses them. Yields the stream."""
-    _check_dev(*ts)
-    dev = next(t.device for t in ts if t is not None)
-    if any(t is not None and t.device != dev for t in ts):
-        raise ValueError("tensors must be on one device")
+def _device_of(*ts):
+    """The one device of these contiguous tensors (None skipped)."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError("tensors must be contiguous device tensors")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("tensors must be on one device")
+    return dev
+
+
+def _on(dev, stream):
+    """(context, stream handle): the context makes the tensors' device and the stream (default: its
+    current one) current, so that results and workspaces allocated inside belong to the stream that
+    uses them."""
     if stream is None:
-        with torch.cuda.device(dev):
-            yield torch.cuda.current_stream()
-    else:
-        if stream.device != dev:
-            raise ValueError("the stream is on another device than the tensors")
-        with torch.cuda.stream(stream):
-            yield stream
+        if dev.index == torch.cuda.current_device():
+            return _NO_CONTEXT, torch.cuda.current_stream(dev).cuda_stream
+        return torch.cuda.device(dev), torch.cuda.current_stream(dev).cuda_stream
+    if stream.device != dev:
+        raise ValueError("the stream is on another device than the tensors")
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+_NO_CONTEXT = contextlib.nullcontext()
 
 
 def _check_tensor(name, t, shape, *dtypes):
-    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
+    if t.shape != shape or t.dtype not in dtypes:
         raise ValueError(f"{name}: expected {tuple(shape)} of {' or '.join(map(str, dtypes))}, got "
                          f"{tuple(t.shape)} of {t.dtype}")
 
@@ -398,11 +410,12 @@ def _grouped(entry, a, b, offsets, R, E, N, K, shape, out, out_dtype, stream):
     _check_tensor("offsets", offsets, (E + 1,), torch.int32)
     if out is not None:
         _check_tensor("out", out, shape, odt)
-    with _placed(stream, a, b, offsets, out) as st:
+    ctx, st = _on(_device_of(a, b, offsets, out), stream)
+    with ctx:
         if out is None:
             out = torch.empty(shape, dtype=odt, device=a.device)
-        rc = getattr(lib(), entry)(_ptr(a), _ptr(b), _ptr(offsets), _ptr(out), R, E, N, K,
-                                   out_dtype, _stream(st))
+        rc = getattr(lib(), entry)(a.data_ptr(), b.data_ptr(), offsets.data_ptr(), out.data_ptr(), R,
+                                   E, N, K, out_dtype, st)
     if rc != 0:
         raise BeamError(rc, entry)
     return out
@@ -450,18 +463,20 @@ def residual_boundary_backward(y, h_out, gamma_post, gamma_next, d_h_out, d_x_ne
     None (no gradient through the residual stream), d_h may be d_h_out (in place)."""
     T, H = h_out.shape
     bf, f32 = torch.bfloat16, torch.float32
-    _check_tensor("y", y, (T, H), bf, f32)
+    shape = h_out.shape
+    _check_tensor("y", y, shape, bf, f32)
     for name, t in (("h_out", h_out), ("d_h_out", d_h_out), ("d_x_next", d_x_next), ("d_h", d_h)):
         if t is not None:
-            _check_tensor(name, t, (T, H), bf)
+            _check_tensor(name, t, shape, bf)
     for name, t in (("gamma_post", gamma_post), ("gamma_next", gamma_next),
                     ("d_gamma_post", d_gamma_post), ("d_gamma_next", d_gamma_next)):
         if t is not None:
             _check_tensor(name, t, (H,), f32)
     if d_y is not None:
         _check_tensor("d_y", d_y, (T, H), y.dtype)
-    with _placed(stream, y, h_out, gamma_post, gamma_next, d_h_out, d_x_next, d_y, d_h, d_gamma_post,
-                 d_gamma_next, workspace) as st:
+    ctx, st = _on(_device_of(y, h_out, gamma_post, gamma_next, d_h_out, d_x_next, d_y, d_h,
+                             d_gamma_post, d_gamma_next, workspace), stream)
+    with ctx:
         d_y = torch.empty_like(y) if d_y is None else d_y
         d_h = torch.empty_like(h_out) if d_h is None else d_h
         # no tokens: the call writes nothing, and the sums over none are zero
@@ -474,10 +489,11 @@ def residual_boundary_backward(y, h_out, gamma_post, gamma_next, d_h_out, d_x_ne
             nbytes = residual_boundary_backward_workspace_bytes(T, H)
             workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=y.device)
         rc = lib().beam_residual_boundary_backward(
-            _ptr(y), _DT_CODE[y.dtype], _ptr(h_out), _ptr(gamma_post), _ptr(gamma_next),
-            _ptr(d_h_out), _ptr(d_x_next), _ptr(d_y), _ptr(d_h), _ptr(d_gamma_post),
-            _ptr(d_gamma_next), T, H, int(depth_n), float(eps), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _stream(st))
+            y.data_ptr(), _DT_CODE[y.dtype], h_out.data_ptr(), gamma_post.data_ptr(),
+            gamma_next.data_ptr(), None if d_h_out is None else d_h_out.data_ptr(),
+            d_x_next.data_ptr(), d_y.data_ptr(), d_h.data_ptr(), d_gamma_post.data_ptr(),
+            d_gamma_next.data_ptr(), T, H, int(depth_n), float(eps), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), st)
     if rc != 0:
         raise BeamError(rc, "beam_residual_boundary_backward")
     return d_y, d_h, d_gamma_post, d_gamma_next
@@ -499,16 +515,16 @@ def orthogonalise(g, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: floa
     if out is not None:
         _check_tensor("out", out, g.shape, torch.bfloat16)
     abc = (ctypes.c_float * 3)(*[float(c) for c in coeffs])
-    with _placed(stream, g, out, workspace) as st:
+    ctx, st = _on(_device_of(g, out, workspace), stream)
+    with ctx:
         if out is None:
             out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
         if workspace is None:
             nbytes = orthogonalise_workspace_bytes(n, rows, cols)
             workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=g.device)
-        rc = lib().beam_moe_orthogonalise(_ptr(g), _DT_CODE[g.dtype], _ptr(out), n, rows, cols,
-                                          int(steps), abc, float(eps), _ptr(workspace),
-                                          workspace.numel() * workspace.element_size(),
-                                          _stream(st))
+        rc = lib().beam_moe_orthogonalise(g.data_ptr(), _DT_CODE[g.dtype], out.data_ptr(), n, rows,
+                                          cols, int(steps), abc, float(eps), workspace.data_ptr(),
+                                          workspace.numel() * workspace.element_size(), st)
     if rc != 0:
         raise BeamError(rc, "beam_moe_orthogonalise")
     return out

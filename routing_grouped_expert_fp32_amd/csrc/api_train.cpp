@@ -101,7 +101,7 @@ beam_status_t beam_moe_grouped_mm_dw(const void* dy, const void* x, const int32_
 
 size_t beam_residual_boundary_backward_workspace_bytes(int64_t T, int32_t hidden) {
   if (T <= 0 || hidden <= 0 || hidden > beam::boundary_max_hidden()) return 0;
-  return sizeof(float) * 2 * (size_t)beam::boundary_bwd_parts(T) * (size_t)hidden;
+  return sizeof(float) * 2 * (size_t)beam::boundary_bwd_parts(T, hidden) * (size_t)hidden;
 }
 
 beam_status_t beam_residual_boundary_backward(

@@ -168,10 +168,10 @@ struct BoundaryBwdArgs {
   uint16_t* d_h;             // [T][H] (may be d_h_in)
   float* d_gamma_post;       // [H]
   float* d_gamma_next;       // [H]
-  float* parts;              // [boundary_bwd_parts(T)][2][H]
+  float* parts;              // [boundary_bwd_parts(T, H)][2][H]
   float alpha, beta, eps;
 };
-int boundary_bwd_parts(int64_t T);
+int boundary_bwd_parts(int64_t T, int H);
 hipError_t launch_boundary_bwd(const BoundaryBwdArgs& a, int64_t T, int H, hipStream_t st);
 
 // Workspace of the orthogonalised update (byte offsets): partial sums of squares, X as hi (two, in

@@ -322,13 +322,6 @@ __device__ __forceinline__ int xcd_tile(int wg, int total) {
   return local < per && v < total ? v : -1;
 }
 
-// Two values rounded to bf16, to nearest even, by one conversion instruction.
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
-}
-
 // Stores a tile's accumulators (NV row sub-tiles a wave): rows m < rows and columns n < cols, cols a
 // multiple of 8, of the tile whose first value is at `out`, `ld` bytes from row to row (a tile's
 // rows under 2 GiB). An instruction writes 64 bytes of each of 16 rows in 16-byte pieces; for bf16
