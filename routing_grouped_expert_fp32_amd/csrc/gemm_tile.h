@@ -30,6 +30,8 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 // Workgroup tile of BM x BN, WM x WN waves; LDS rings of AST stages of the A operand and BST of B
 // (AST <= BST: B is the one that streams from HBM, A's rows are shared by neighbouring tiles), of KT
 // values of k each.
+// Row sub-tiles (16 rows) are dealt to the wave rows in turn, so that a partly filled tile loads them
+// alike.
 template <int BM_, int BN_, int WM_, int WN_, int AST_, int BST_, int KT_ = 64>
 struct TileShape {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, AST = AST_, BST = BST_, KT = KT_;
@@ -41,6 +43,8 @@ struct TileShape {
   static constexpr int kLdsBytes = AST * kABytes + BST * kBBytes;
   static_assert(kLdsBytes <= 160 * 1024, "LDS budget");
   static_assert(FM * 16 * WM == BM && FN * 16 * WN == BN, "whole sub-tiles");
+  // sub-tile i of wave row wm
+  __device__ static constexpr int row_tile(int wm, int i) { return wm + WM * i; }
 };
 
 // Wave-uniform values that the compiler would otherwise keep in vector registers, where a buffer
@@ -181,7 +185,7 @@ __device__ __forceinline__ void tile_barrier() {
 }
 
 // One wave's side of a stage: its fragments and their schedule. A stage is NV positions a step: position p
-// multiplies row sub-tile p % NV in step p / NV; acc[i][j] is sub-tile (wm + WM i, wn FN + j). NV of
+// multiplies row sub-tile p % NV in step p / NV; acc[i][j] is sub-tile (row_tile(wm, i), wn FN + j). NV of
 // the wave's FM row sub-tiles hold rows, the others' accumulators are left alone.
 //
 // Fragments are read ahead of their MFMAs, the row operand's AHEAD positions, the other's one step.
@@ -196,7 +200,7 @@ struct TileStage {
   intx4 af[P + AHEAD], bf[STEPS + 1][S::FN];   // the next stage's first ones at the end
 
   __device__ __forceinline__ void init(int wave, int lane) {
-    ra.init(wave / S::WN, lane);
+    ra.init(S::row_tile(wave / S::WN, 0), lane);
     rb.init(wave % S::WN * S::FN, lane);
   }
   // the first fragments of the first stage, which has landed in the slots sa, sb
@@ -303,18 +307,6 @@ __device__ __forceinline__ void tile_kloop(const OperandLoader<S::BM, S::kWaves,
   }
 }
 
-// Walks a tile's accumulators: f(m, n, v) with v = D[m][n .. n + 3], m and n within the tile.
-template <class S, int NV, class F>
-__device__ __forceinline__ void tile_for_each(const floatx4 (&acc)[S::FM][S::FN], int wave,
-                                              int lane, F&& f) {
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < S::FN; ++j)
-      f(16 * (wave / S::WN + S::WM * i) + (lane & 15),
-        16 * (wave % S::WN * S::FN + j) + 4 * (lane >> 4), acc[i][j]);
-}
-
 // Tile v of `total` for workgroup `wg` of a grid of 8 ceil(total / 8), one run of tiles per XCD.
 __device__ __forceinline__ int xcd_tile(int wg, int total) {
   const int per = (total + 7) >> 3, local = wg >> 3;
@@ -322,48 +314,63 @@ __device__ __forceinline__ int xcd_tile(int wg, int total) {
   return local < per && v < total ? v : -1;
 }
 
-// Stores a tile's accumulators (NV row sub-tiles a wave): rows m < rows and columns n < cols, cols a
-// multiple of 8, of the tile whose first value is at `out`, `ld` bytes from row to row (a tile's
-// rows under 2 GiB). An instruction writes 64 bytes of each of 16 rows in 16-byte pieces; for bf16
-// that takes two neighbouring sub-tiles, whose halves a lane swaps with the lane 16 away (64-byte
-// runs of plain stores fill memory at 5.4 TB/s, the 32-byte runs of one bf16 sub-tile at 4.4;
-// non-temporal stores of less than whole lines at 2 - 3). Lanes outside are dropped by the buffer's
-// bounds.
+// Hands a tile's accumulators (NV row sub-tiles a wave) on in row order: put(i, j, p) writes the lane's
+// four values of acc[i][j] (column 16 j + 4 (lane / 16) of the wave's columns) to LDS at p, kSize
+// bytes each, and get(m, n, p) takes the 16 bytes at p, the values of row m from column n on (of the
+// tile). A wave's rows of one sub-tile lie in LDS as 16 rows 16 bytes apart from a multiple of
+// 256 (no bank conflicts); `smem` is the tile's ring, which nobody reads or fills any more: the last
+// stage's barrier stands behind its last reads.
+//
+// A CU stores 35 GB/s in runs of 64 bytes, as the accumulators lie, and 140 GB/s in long rows: a
+// 256 x 256 fp32 tile takes 7.3 us or 1.9 (measured with one workgroup a CU, 8 to 256 CUs).
+template <class S, int NV, int kSize, class Put, class Get>
+__device__ __forceinline__ void tile_rows(unsigned char* smem, int wave, int lane, Put&& put,
+                                          Get&& get) {
+  constexpr int kRow = S::FN * 16 * kSize, kPitch = kRow + 16, kBuf = 16 * kPitch;
+  static_assert(S::kWaves * 2 * kBuf <= S::kLdsBytes, "staging fits the ring");
+  constexpr int kChunks = kRow / 16, kRows = 64 / kChunks;   // of a row; rows an instruction
+  static_assert(kChunks <= 64 && 16 % kRows == 0, "whole rows");
+  unsigned char* const mine = smem + wave * 2 * kBuf;
+  const int wm = wave / S::WN, wn = wave % S::WN;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    unsigned char* const buf = mine + (i & 1) * kBuf;
+#pragma unroll
+    for (int j = 0; j < S::FN; ++j)
+      put(i, j, buf + (lane & 15) * kPitch + (16 * j + 4 * (lane >> 4)) * kSize);
+#pragma unroll
+    for (int p = 0; p < 16 / kRows; ++p) {
+      const int r = p * kRows + lane / kChunks, c = lane % kChunks;
+      get(16 * S::row_tile(wm, i) + r, wn * S::FN * 16 + c * (16 / kSize), buf + r * kPitch + 16 * c);
+    }
+  }
+}
+
+// Stores a tile's accumulators: rows m < rows and columns n < cols, cols a multiple of 8, of the tile
+// whose first value is at `out`, `ld` bytes from row to row (a tile's rows under 2 GiB). Lanes
+// outside are dropped by the buffer's bounds.
 template <class S, int NV, bool OUT_BF16>
 __device__ __forceinline__ void tile_store(const floatx4 (&acc)[S::FM][S::FN], void* out, int64_t ld,
-                                           int rows, int cols, int wave, int lane) {
-  static_assert(S::FN % 2 == 0, "sub-tiles in pairs");
+                                           int rows, int cols, unsigned char* smem, int wave,
+                                           int lane) {
   constexpr int kSize = OUT_BF16 ? 2 : 4;
-  const int m0 = 16 * (wave / S::WN) + (lane & 15), g = lane >> 4;
-  // bf16: lanes g = 0, 2 take columns 0-7, 8-15 of the pair's first sub-tile, g = 1, 3 of its second
-  const int n0 = 16 * (wave % S::WN * S::FN) + (OUT_BF16 ? 16 * (g & 1) + 4 * (g & 2) : 4 * g);
   const uint32_t bytes = (uint32_t)((min(rows, S::BM) - 1) * ld + min(cols, S::BN) * kSize);
   const auto rsrc =
       __builtin_amdgcn_make_buffer_rsrc(uniform(out), (short)0, uniform((int)bytes), 0x00020000);
-  const uint32_t v0 = (uint32_t)(m0 * ld + n0 * kSize);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const bool in_row = m0 + 16 * S::WM * i < rows;
-    const uint32_t row = (uint32_t)(16 * S::WM * i * ld);
-#pragma unroll
-    for (int j = 0; j < S::FN; j += OUT_BF16 ? 2 : 1) {
-      // outside: past the buffer whichever way its range check counts the scalar offset
-      const uint32_t voff = in_row && n0 + 16 * j < cols ? v0 : 0x80000000u;
-      const uint32_t soff = row + 16 * j * kSize;
-      u32x4 o;
-      if constexpr (OUT_BF16) {
-        const floatx4 v = acc[i][j], w = acc[i][j + 1];
-        const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16(v.x, v.y), pack_bf16(w.x, w.y),
-                                                        false, false);
-        const auto y = __builtin_amdgcn_permlane16_swap(pack_bf16(v.z, v.w), pack_bf16(w.z, w.w),
-                                                        false, false);
-        o = u32x4{x[0], y[0], x[1], y[1]};
-      } else {
-        o = __builtin_bit_cast(u32x4, acc[i][j]);
-      }
-      __builtin_amdgcn_raw_buffer_store_b128(o, rsrc, voff, soff, 0);
-    }
-  }
+  tile_rows<S, NV, kSize>(
+      smem, wave, lane,
+      [&](int i, int j, unsigned char* p) {
+        const floatx4 v = acc[i][j];
+        if constexpr (OUT_BF16)
+          *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)};
+        else
+          *reinterpret_cast<floatx4*>(p) = v;
+      },
+      [&](int m, int n, const unsigned char* p) {
+        const uint32_t off = (uint32_t)(m * ld + n * kSize);
+        __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4*>(p), rsrc,
+                                               m < rows && n < cols ? off : 0x80000000u, 0, 0);
+      });
 }
 
 }  // namespace beam

@@ -154,7 +154,7 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
     tile_kloop<S, false, WCOL, false, NV>(la, lb, Kc, smem, wave, lane, acc);
     constexpr int kSize = OUT_BF16 ? 2 : 4;
     tile_store<S, NV, OUT_BF16>(acc, out + ((int64_t)blk.row0 * No + col0) * kSize,
-                                (int64_t)No * kSize, blk.rows, No - col0, wave, lane);
+                                (int64_t)No * kSize, blk.rows, No - col0, smem, wave, lane);
   };
   if (S::FM > 8 && nv > 8)
     body(std::integral_constant<int, S::FM>{});
@@ -201,7 +201,7 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   tile_kloop<S, true, true, false, S::FM>(la, lb, end - begin, smem, wave, lane, acc);
   constexpr int kSize = OUT_BF16 ? 2 : 4;
   tile_store<S, S::FM, OUT_BF16>(acc, dw + (((int64_t)e * N + row0) * K + col0) * kSize,
-                                 (int64_t)K * kSize, N - row0, K - col0, wave, lane);
+                                 (int64_t)K * kSize, N - row0, K - col0, smem, wave, lane);
 }
 
 // Tiles of the forward and the input gradient, by the mean number of rows of an expert (the counts

@@ -185,10 +185,10 @@ __device__ __forceinline__ void triangle_tile(int t, int& i, int& j) {
 }
 
 // D = X X^T of `x` [m][ld] (contraction over k values of each row): tiles on or under the diagonal,
-// written to both halves of out [m][mp].
+// written to both halves of out [m][mp], the mirrored one in 8-byte pieces after a 4 x 4 transpose
+// between neighbouring lanes (both halves through LDS in long rows: 14 us a 256 x 256 tile slower).
 //   POLY = false: out = D * c0                               (x = hi: A)
 //   POLY = true:  out = b x + D * c0 + ident on the diagonal (x = A:  B + s I)
-// The mirrored half goes out in 8-byte pieces after a 4 x 4 transpose between neighbouring lanes.
 template <class S, bool POLY>
 __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) void ns_gram_kernel(
     const _Float16* __restrict__ x, _Float16* __restrict__ out, int m, int mp, int ld, int k,
@@ -227,7 +227,7 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
       for (int i = 0; i < kBatch; ++i)
 #pragma unroll
         for (int j = 0; j < S::FN; ++j) {
-          const int r = row0 + 16 * (wave / S::WN + S::WM * (i0 + i)) + (lane & 15);
+          const int r = row0 + 16 * S::row_tile(wave / S::WN, i0 + i) + (lane & 15);
           const int c = dn0 + 16 * j;
           // outside the matrix any value inside it does: its result is not stored
           a[i][j] = *reinterpret_cast<const f16x4*>(xm + (int64_t)min(r, m - 1) * ld +
@@ -238,7 +238,7 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
     for (int i = 0; i < kBatch; ++i)
 #pragma unroll
       for (int j = 0; j < S::FN; ++j) {
-        const int r = row0 + 16 * (wave / S::WN + S::WM * (i0 + i)) + (lane & 15);
+        const int r = row0 + 16 * S::row_tile(wave / S::WN, i0 + i) + (lane & 15);
         const int c = dn0 + 16 * j;
         floatx4 v = acc[i0 + i][j] * c0;   // zero in rows and columns from m on
         if constexpr (POLY) {
@@ -285,9 +285,12 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   tile_zero<S>(acc);
   tile_kloop<S, false, false, true, S::FM>(la, lb, min(kp, k - part * kp), smem, wave, lane, acc);
   float* o = sums + (int64_t)blockIdx.x * (S::BM * S::BN);
-  tile_for_each<S, S::FM>(acc, wave, lane, [&](int dm, int dn, floatx4 d) {
-    *reinterpret_cast<floatx4*>(o + dm * S::BN + dn) = d;
-  });
+  tile_rows<S, S::FM, 4>(
+      smem, wave, lane,
+      [&](int i, int j, unsigned char* p) { *reinterpret_cast<floatx4*>(p) = acc[i][j]; },
+      [&](int m, int n, const unsigned char* p) {
+        *reinterpret_cast<floatx4*>(o + m * S::BN + n) = *reinterpret_cast<const floatx4*>(p);
+      });
 }
 
 // A = c0 * the parts' sum, in part order, to both halves. A workgroup per quarter of a tile.
@@ -351,71 +354,64 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   floatx4 acc[S::FM][S::FN];
   tile_zero<S>(acc);
   tile_kloop<S, false, true, true, S::FM>(la, lb, m, smem, wave, lane, acc);
-  // two neighbouring sub-tiles at a time: after a swap with the lane 16 away a lane has eight
-  // consecutive columns of one of them (lanes g = 0, 2: the first, g = 1, 3: the second)
-  const int g = lane >> 4;
-  const int c0 = col0 + 16 * (wave % S::WN * S::FN + (g & 1)) + 4 * (g & 2);
-  constexpr int kBatch = S::FM / 4;   // row sub-tiles whose hi and lo are read together
+  // in row order, four values a lane; hi and lo of the next two sub-tiles' rows are under way while
+  // one's are used
+  constexpr int kChunks = S::FN * 4, kRows = 64 / kChunks, kParts = 16 / kRows;
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  const int dr = lane / kChunks, c = col0 + wn * S::FN * 16 + lane % kChunks * 4;
+  auto place = [&](int i, int p) {   // clamped into the matrix; outside, the result is not stored
+    const int r = row0 + 16 * S::row_tile(wm, i) + p * kRows + dr;
+    return x0 + (int64_t)min(r, m - 1) * ld + min(c, ld - 4);
+  };
+  f16x4 h[S::FM][kParts], l[S::FM][kParts];
+  auto fetch = [&](int i) {
 #pragma unroll
-  for (int i0 = 0; i0 < S::FM; i0 += kBatch) {
-    f16x8 h[kBatch][S::FN / 2], l[kBatch][S::FN / 2];
+    for (int p = 0; p < kParts; ++p) {
+      h[i][p] = *reinterpret_cast<const f16x4*>(hi + place(i, p));
+      l[i][p] = *reinterpret_cast<const f16x4*>(lo + place(i, p));
+    }
+  };
+  constexpr int kAhead = S::FM < 2 ? S::FM : 2;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
+  for (int i = 0; i < kAhead; ++i) fetch(i);
+  int step = 0;   // sub-tile and part that the next get is for: get is called in that order
+  tile_rows<S, S::FM, 4>(
+      smem, wave, lane,
+      [&](int i, int j, unsigned char* p) {
+        if (j == 0 && i + kAhead < S::FM) fetch(i + kAhead);
+        *reinterpret_cast<floatx4*>(p) = acc[i][j];
+      },
+      [&](int dm, int dn, const unsigned char* p) {
+        const int i = step / kParts, part = step % kParts;
+        ++step;
+        const int r = row0 + dm;
+        floatx4 v = *reinterpret_cast<const floatx4*>(p);
+        const f16x4 hv = h[i][part], lv = l[i][part];
+        if (r >= m || c >= ld) return;   // ld % 8 == 0: four columns are all in or all out
 #pragma unroll
-      for (int j = 0; j < S::FN / 2; ++j) {
-        const int r = row0 + 16 * (wave / S::WN + S::WM * (i0 + i)) + (lane & 15);
-        // outside the matrix any value inside it does: its result is not stored
-        const int64_t at = x0 + (int64_t)min(r, m - 1) * ld + min(c0 + 32 * j, ld - 8);
-        h[i][j] = load_f16x8(hi + at);
-        l[i][j] = load_f16x8(lo + at);
-      }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-      for (int j = 0; j < S::FN / 2; ++j) {
-        const int r = row0 + 16 * (wave / S::WN + S::WM * (i0 + i)) + (lane & 15);
-        const int c = c0 + 32 * j;
-        float d[8];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const auto sw = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i0 + i][2 * j][q]),
-                                                           __float_as_uint(acc[i0 + i][2 * j + 1][q]),
-                                                           false, false);
-          d[q] = __uint_as_float(sw[0]);
-          d[q + 4] = __uint_as_float(sw[1]);
-        }
-        if (r >= m || c >= ld) continue;   // ld % 8 == 0: eight columns are all in or all out
-        const int64_t at = x0 + (int64_t)r * ld + c;
-        // zero in columns n .. ld - 1
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          d[q] = c_prod * d[q] + c_hi * (float)h[i][j][q] + c_lo * (float)l[i][j][q];
+        for (int q = 0; q < 4; ++q)   // zero in columns n .. ld - 1
+          v[q] = c_prod * v[q] + c_hi * (float)hv[q] + c_lo * (float)lv[q];
         if constexpr (!LAST) {
-          f16x8 nh, nl;
+          const int64_t at = x0 + (int64_t)r * ld + c;
+          const f16x4 nh{(_Float16)v.x, (_Float16)v.y, (_Float16)v.z, (_Float16)v.w};
+          f16x4 nl;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            nh[q] = (_Float16)d[q];
-            nl[q] = (_Float16)(d[q] - (float)nh[q]);
-          }
-          *reinterpret_cast<f16x8*>(hi_out + at) = nh;
-          *reinterpret_cast<f16x8*>(lo + at) = nl;
+          for (int q = 0; q < 4; ++q) nl[q] = (_Float16)(v[q] - (float)nh[q]);
+          *reinterpret_cast<f16x4*>(hi_out + at) = nh;
+          *reinterpret_cast<f16x4*>(lo + at) = nl;
+        } else if (!tall && (n & 3) == 0) {   // 8-byte aligned rows, four columns in or out
+          if (c < n)
+            *reinterpret_cast<u32x2*>(out + ((int64_t)mat * m + r) * n + c) =
+                u32x2{pack_bf16(c_out * v.x, c_out * v.y), pack_bf16(c_out * v.z, c_out * v.w)};
         } else {
           uint16_t* o = out + (int64_t)mat * m * n;
-          if (!tall && (n & 7) == 0) {
-            u32x4 w;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) w[q] = pack_bf16(c_out * d[2 * q], c_out * d[2 * q + 1]);
-            *reinterpret_cast<u32x4*>(o + (int64_t)r * n + c) = w;
-          } else {
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              if (c + q < n)
-                o[tall ? (int64_t)(c + q) * m + r : (int64_t)r * n + c + q] =
-                    (uint16_t)pack_bf16(c_out * d[q], 0.f);
-          }
+          for (int q = 0; q < 4; ++q)
+            if (c + q < n)
+              o[tall ? (int64_t)(c + q) * m + r : (int64_t)r * n + c + q] =
+                  (uint16_t)pack_bf16(c_out * v[q], 0.f);
         }
-      }
-  }
+      });
 }
 
 // ---- host side -----------------------------------------------------------------------------------
