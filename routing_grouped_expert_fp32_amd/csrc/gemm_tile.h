@@ -79,7 +79,7 @@ struct OperandLoader {
   static_assert(COL || KT == 64, "the swizzle of row operands is made for 128-byte rows");
   static constexpr int kRowChunks = COL ? ROWS / 8 : 8;       // 16-byte chunks of a stored row
   static constexpr int kLoadRows = 64 / kRowChunks;           // stored rows of a load
-  static_assert(!COL || ROWS >= 64, "the swizzle needs four 32-byte units a row");
+  static_assert(!COL || (ROWS >= 64 && (ROWS & (ROWS - 1)) == 0), "the swizzle permutes 4 or 8 units");
   TileOperand op;
   uint32_t voff[L];
   bool stream = false;   // read once: non-temporal loads
@@ -269,7 +269,9 @@ __device__ __forceinline__ void tile_kloop(const OperandLoader<S::BM, S::kWaves,
   constexpr int LA = OperandLoader<S::BM, S::kWaves, ACOL, S::KT>::L;
   constexpr int LB = OperandLoader<S::BN, S::kWaves, BCOL, S::KT>::L;
   static_assert(S::BST * (LA + LB) < 64, "vmcnt range");
-  // a wave's loads are issued, and counted, in the order A(t), B(t + BST - AST)
+  // a wave's loads are issued, and counted, in the order A(t), B(t + BST - AST): behind the loads of
+  // stage t + 1 came B's of that turn, if B runs ahead, and both operands' of AST - 2 turns
+  constexpr int kBehind = (S::AST - 2) * (LA + LB) + (S::BST > S::AST ? LB : 0);
   auto issue_a = [&](int st) { la.issue(st, k, aring + (st % S::AST) * S::kABytes, wave); };
   auto issue_b = [&](int st) { lb.issue(st, k, bring + (st % S::BST) * S::kBBytes, wave); };
 #pragma unroll
@@ -293,8 +295,7 @@ __device__ __forceinline__ void tile_kloop(const OperandLoader<S::BM, S::kWaves,
               [&]() {
                 // own reads of this stage are done; own loads of the next one have landed
                 if (kt + S::BST <= nk)
-                  __builtin_amdgcn_s_waitcnt(
-                      vmcnt_imm((S::AST - 2) * LA + (S::BST - 2) * LB) & kLgkmZero);
+                  __builtin_amdgcn_s_waitcnt(vmcnt_imm(kBehind) & kLgkmZero);
                 else
                   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0) & kLgkmZero);
                 tile_barrier();
@@ -328,8 +329,11 @@ __device__ __forceinline__ void tile_rows(unsigned char* smem, int wave, int lan
                                           Get&& get) {
   constexpr int kRow = S::FN * 16 * kSize, kPitch = kRow + 16, kBuf = 16 * kPitch;
   static_assert(S::kWaves * 2 * kBuf <= S::kLdsBytes, "staging fits the ring");
-  constexpr int kChunks = kRow / 16, kRows = 64 / kChunks;   // of a row; rows an instruction
-  static_assert(kChunks <= 64 && 16 % kRows == 0, "whole rows");
+  // lanes of a row (the last ones idle where its chunks are no power of two), rows an instruction
+  constexpr int kChunks = kRow / 16;
+  constexpr int kLanes = kChunks <= 4 ? 4 : kChunks <= 8 ? 8 : kChunks <= 16 ? 16 : 32;
+  constexpr int kRows = 64 / kLanes;
+  static_assert(kChunks <= kLanes && kRows <= 16, "whole rows");
   unsigned char* const mine = smem + wave * 2 * kBuf;
   const int wm = wave / S::WN, wn = wave % S::WN;
 #pragma unroll
@@ -340,8 +344,10 @@ __device__ __forceinline__ void tile_rows(unsigned char* smem, int wave, int lan
       put(i, j, buf + (lane & 15) * kPitch + (16 * j + 4 * (lane >> 4)) * kSize);
 #pragma unroll
     for (int p = 0; p < 16 / kRows; ++p) {
-      const int r = p * kRows + lane / kChunks, c = lane % kChunks;
-      get(16 * S::row_tile(wm, i) + r, wn * S::FN * 16 + c * (16 / kSize), buf + r * kPitch + 16 * c);
+      const int r = p * kRows + lane / kLanes, c = lane % kLanes;
+      if (kChunks == kLanes || c < kChunks)
+        get(16 * S::row_tile(wm, i) + r, wn * S::FN * 16 + c * (16 / kSize),
+            buf + r * kPitch + 16 * c);
     }
   }
 }

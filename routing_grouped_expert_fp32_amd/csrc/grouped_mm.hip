@@ -205,23 +205,25 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
 }
 
 // Tiles of the forward and the input gradient, by the mean number of rows of an expert (the counts
-// themselves are on the device). Measured at 32 experts of 5120 x 5120 (us, forward; a 1.68 GB read
-// of the weights alone takes about 260):
-//   rows / expert         1    64   110   156   256
-//   32 x 128  (4, 4)    173    443
-//   128 x 256 (2, 3)           308   324   433
-//   192 x 256 (2, 3)           311   323   350
-//   320 x 256 (2, 2)           381   384   396   447
-//   256 x 256 (2, 2)                               564
+// themselves are on the device). Measured at 32 experts of 5120 x 5120 (us, forward; reading the
+// 1.68 GB of weights alone takes about 260):
+//   rows / expert         1    64   110   156   219   256
+//   32 x 128  (4, 4)    173   443
+//   128 x 256 (2, 3)          308   324   433
+//   192 x 256 (2, 3)          311   323   350
+//   256 x 256 (2, 3)                      414   567
+//   320 x 256 (2, 2)          381   384   396   443   454
 // Few rows: narrow tiles, many workgroups streaming weights. More: one block an expert if it can be,
-// as every further block reads the weights again; the B operand's third stage covers their latency
-// while LDS lasts. Past 1536 rows blocks are many anyway and 256 x 256 multiplies fastest (one
-// matrix of 8192 x 8192, 8192 rows: 794 us, 320 x 256 895). Where a tile leaves CUs without work,
-// 64 x 64: 523 rows, 16 experts of 776 x 520, 6.9 us (128 x 128 tiles 12.3).
+// as every further block reads the weights again (counts spread by about the square root of their
+// mean: 2.5 of it are allowed for); the B operand's third stage covers their latency while LDS
+// lasts. Past 1536 rows blocks are many anyway and 256 x 256 multiplies fastest (one matrix of 8192
+// x 8192, 8192 rows: 790 us, 320 x 256 895). Where a tile leaves CUs without work, 64 x 64: 523
+// rows, 16 experts of 776 x 520, 6.9 us (128 x 128 tiles 12.3).
 using TileStream = TileShape<32, 128, 1, 4, 4, 4>;
 using Tile64 = TileShape<64, 64, 1, 2, 3, 3>;
 using Tile128 = TileShape<128, 256, 2, 4, 2, 3>;
 using Tile192 = TileShape<192, 256, 2, 4, 2, 3>;
+using Tile256Deep = TileShape<256, 256, 2, 4, 2, 3>;
 using Tile256 = TileShape<256, 256, 2, 4, 2, 2>;
 using Tile320 = TileShape<320, 256, 2, 4, 2, 2>;
 constexpr int kGroupedCus = 256;
@@ -232,12 +234,18 @@ static void with_rows_tile(int64_t R, int64_t E, int64_t No, F&& f) {
   auto fits = [&](int64_t bm, int64_t bn) {
     return full * ceil_div(mean, bm) * ceil_div(No, bn) >= kGroupedCus;
   };
+  // mean + 2.5 sqrt(mean) <= bm
+  auto one_block = [&](int64_t bm) {
+    return mean <= bm && 4 * (bm - mean) * (bm - mean) >= 25 * mean;
+  };
   if (mean <= 24 && fits(32, 128))
     f(TileStream{});
-  else if (mean <= 112 && fits(128, 256))
+  else if (one_block(128) && fits(128, 256))
     f(Tile128{});
-  else if (mean <= 192 && fits(192, 256))
+  else if (one_block(192) && fits(192, 256))
     f(Tile192{});
+  else if (one_block(256) && fits(256, 256))
+    f(Tile256Deep{});
   else if (mean <= 1536 && fits(320, 256))
     f(Tile320{});
   else if (fits(256, 256))

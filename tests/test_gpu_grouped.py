@@ -103,6 +103,36 @@ def test_against_oracle(op, out_dtype, counts, N, K):
     check(op, counts, N, K, out_dtype, False, seed=3)
 
 
+# calls large enough for each of the wide tiles: (experts, mean rows, output width, contraction)
+TILES = [(40, 10, 904, 72), (33, 24, 1032, 200), (32, 70, 2056, 72), (32, 150, 2056, 136),
+         (32, 208, 2184, 72), (16, 300, 2056, 264), (16, 700, 1288, 72), (3, 1700, 3336, 72)]
+
+
+@pytest.mark.parametrize("op", ["mm", "dx"])
+@pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("E,mean,width,depth", TILES)
+def test_exact_sums_wide_tiles(op, out_dtype, E, mean, width, depth):
+    rng = np.random.default_rng(E * mean)
+    counts = rng.multinomial(E * mean, rng.dirichlet(np.full(E, 20.0)))
+    counts[E // 2] = 0
+    N, K = (width, depth) if op == "mm" else (depth, width)
+    check(op, counts.tolist(), N, K, out_dtype, True, first=3, behind=5, seed=E)
+
+
+@pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("counts,N,K", [([0, 1, 63, 64, 65, 128, 300] * 4, 1032, 776),
+                                        ([1000], 4104, 4112), ([40] * 65, 520, 264)])
+def test_exact_sums_weight_gradient_tiles(out_dtype, counts, N, K):
+    check("dw", counts, N, K, out_dtype, True, first=2, behind=1)
+
+
+@pytest.mark.parametrize("op", ["mm", "dx", "dw"])
+def test_many_experts(op):
+    counts = np.zeros(4096, dtype=int)
+    counts[[0, 63, 64, 65, 1000, 4095]] = [3, 1, 2, 40, 7, 5]
+    check(op, counts.tolist(), 64, 72, "f32", True)
+
+
 @pytest.mark.parametrize("op", ["mm", "dx"])
 def test_rows_outside_the_offsets_are_left(op):
     counts, N, K, first, behind = [5, 0, 33], 72, 136, 7, 11
