@@ -315,6 +315,35 @@ __device__ __forceinline__ int xcd_tile(int wg, int total) {
   return local < per && v < total ? v : -1;
 }
 
+// The same where tiles 256 columns wide have a CU each: a last round of at most half an XCD's CUs would
+// leave the others idle, so its tiles are split into two column halves (`half` 0 or 1, else -1),
+// which take about 0.6 of a tile's time. Two and a half rounds of 320 x 256 tiles: 467 us as three,
+// 447 with halves.
+constexpr int kXcdCus = 32;
+template <class S>
+using HalfTile = TileShape<S::BM, S::BN / 2, S::WM, S::WN, S::AST, S::BST, S::KT>;
+template <class S>
+constexpr bool kHalves = S::BN == 256 && S::kLdsBytes > 80 * 1024;
+template <class S>
+__device__ __forceinline__ int xcd_tile_halves(int wg, int total, int& half) {
+  const int per = (total + 7) >> 3, first = (wg & 7) * per;
+  const int mine = min(per, total - first);   // tiles of this XCD
+  int local = wg >> 3;
+  half = -1;
+  if constexpr (kHalves<S>) {
+    const int tail = mine % kXcdCus, whole = mine - tail;
+    if (mine > 0 && tail <= kXcdCus / 2 && local >= whole) {
+      half = (local - whole) & 1;
+      local = whole + ((local - whole) >> 1);
+    }
+  }
+  return local < mine ? first + local : -1;
+}
+template <class S>
+static dim3 xcd_grid_halves(int64_t tiles) {
+  return dim3((unsigned)(8 * (ceil_div(tiles, 8) + (kHalves<S> ? kXcdCus / 2 : 0))));
+}
+
 // Hands a tile's accumulators (NV row sub-tiles a wave) on in row order: put(i, j, p) writes the lane's
 // four values of acc[i][j] (column 16 j + 4 (lane / 16) of the wave's columns) to LDS at p, kSize
 // bytes each, and get(m, n, p) takes the 16 bytes at p, the values of row m from column n on (of the

@@ -99,37 +99,13 @@ struct BlockScan {
 
 constexpr int kTileGroup = 4;   // blocks of one expert walked together, column tile by column tile
 
-// out[row][0 .. No) = a[row][0 .. Kc) . w[e], w stored [No][Kc] (forward) or, WCOL, [Kc][No] (input
-// gradient: the weight's rows run across the contraction).
+// One tile: rows of `blk`, columns from col0 on.
 template <class S, bool WCOL, bool OUT_BF16>
-__global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) void grouped_rows_kernel(
-    const unsigned char* __restrict__ a, const unsigned char* __restrict__ w,
-    const int32_t* __restrict__ offsets, unsigned char* __restrict__ out, int R, int E, int No, int Kc,
-    int n_ctiles, int max_blocks) {
-  __shared__ __attribute__((aligned(16))) unsigned char smem[S::kLdsBytes];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  BlockScan<S::BM> scan;
-  scan.init(offsets, E, R, lane);
-  // more blocks than the grid has come only from offsets that are not in order
-  const int v = xcd_tile(blockIdx.x, min(scan.total, max_blocks) * n_ctiles);
-  if (v < 0) return;
-  // an expert's blocks in groups of kTileGroup, column-tile major inside a group: the blocks that
-  // read one weight tile run side by side
-  RowBlock blk = scan.find(v / n_ctiles);
-  if (blk.rows <= 0) return;
-  int ctile;
-  {
-    const int g0 = blk.in_expert - blk.in_expert % kTileGroup;
-    const int sz = min(kTileGroup, blk.n_blocks - g0);
-    const int at = v - (v / n_ctiles - (blk.in_expert - g0)) * n_ctiles;   // tile within the group
-    ctile = at / sz;
-    int lo, hi;
-    expert_rows(offsets, blk.e, R, lo, hi);
-    blk.row0 = lo + (g0 + at % sz) * S::BM;
-    blk.rows = min(S::BM, hi - blk.row0);
-  }
-  const int col0 = ctile * S::BN;
+__device__ __forceinline__ void grouped_rows_tile(const unsigned char* __restrict__ a,
+                                                  const unsigned char* __restrict__ w,
+                                                  unsigned char* __restrict__ out,
+                                                  const RowBlock& blk, int col0, int No, int Kc,
+                                                  unsigned char* smem, int wave, int lane) {
   const int64_t wbytes = (int64_t)No * Kc * 2;
   const int64_t a_ld = (int64_t)Kc * 2;
   OperandLoader<S::BM, S::kWaves, false, S::KT> la;
@@ -166,6 +142,50 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
     body(std::integral_constant<int, S::FM < 4 ? S::FM : 4>{});
   else
     body(std::integral_constant<int, 2>{});
+}
+
+// out[row][0 .. No) = a[row][0 .. Kc) . w[e], w stored [No][Kc] (forward) or, WCOL, [Kc][No] (input
+// gradient: the weight's rows run across the contraction).
+template <class S, bool WCOL, bool OUT_BF16>
+__global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) void grouped_rows_kernel(
+    const unsigned char* __restrict__ a, const unsigned char* __restrict__ w,
+    const int32_t* __restrict__ offsets, unsigned char* __restrict__ out, int R, int E, int No, int Kc,
+    int n_ctiles, int max_blocks) {
+  __shared__ __attribute__((aligned(16))) unsigned char smem[S::kLdsBytes];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  BlockScan<S::BM> scan;
+  scan.init(offsets, E, R, lane);
+  // more blocks than the grid has come only from offsets that are not in order
+  const int total = min(scan.total, max_blocks) * n_ctiles;
+  int half;
+  const int v = xcd_tile_halves<S>(blockIdx.x, total, half);
+  if (v < 0) return;
+  // an expert's blocks in groups of kTileGroup, column-tile major inside a group: the blocks that
+  // read one weight tile run side by side
+  RowBlock blk = scan.find(v / n_ctiles);
+  if (blk.rows <= 0) return;
+  int ctile;
+  {
+    const int g0 = blk.in_expert - blk.in_expert % kTileGroup;
+    const int sz = min(kTileGroup, blk.n_blocks - g0);
+    const int at = v - (v / n_ctiles - (blk.in_expert - g0)) * n_ctiles;   // tile within the group
+    ctile = at / sz;
+    int lo, hi;
+    expert_rows(offsets, blk.e, R, lo, hi);
+    blk.row0 = lo + (g0 + at % sz) * S::BM;
+    blk.rows = min(S::BM, hi - blk.row0);
+  }
+  const int col0 = ctile * S::BN;
+  if constexpr (kHalves<S>) {
+    if (half >= 0) {
+      if (col0 + half * (S::BN / 2) < No)
+        grouped_rows_tile<HalfTile<S>, WCOL, OUT_BF16>(a, w, out, blk, col0 + half * (S::BN / 2), No,
+                                                       Kc, smem, wave, lane);
+      return;
+    }
+  }
+  grouped_rows_tile<S, WCOL, OUT_BF16>(a, w, out, blk, col0, No, Kc, smem, wave, lane);
 }
 
 // dw[e] (N x K) = dy_e^T x_e: both operands lie across the contraction (the expert's rows).
@@ -263,7 +283,7 @@ bool grouped_grid_fits(int64_t R, int64_t E, int64_t N, int64_t K) {
   for (int64_t width : {N, K})
     with_rows_tile(R, E, width, [&](auto s) {
       using S = decltype(s);
-      ok = ok && max_blocks(R, E, S::BM) * ceil_div(width, S::BN) < lim;
+      ok = ok && max_blocks(R, E, S::BM) * ceil_div(width, S::BN) < lim - 8 * kXcdCus;
     });
   return ok;
 }
@@ -275,7 +295,7 @@ hipError_t launch_grouped_rows(const void* a, const void* w, const int32_t* offs
     using S = decltype(s);
     const int64_t blocks = max_blocks(R, E, S::BM);
     const int n_ctiles = (int)ceil_div(No, S::BN);
-    const dim3 grid((unsigned)(8 * ceil_div(blocks * n_ctiles, 8)));
+    const dim3 grid = xcd_grid_halves<S>(blocks * n_ctiles);
     auto go = [&](auto across, auto bf16) {
       hipLaunchKernelGGL((grouped_rows_kernel<S, decltype(across)::value, decltype(bf16)::value>),
                          grid, dim3(S::kThreads), 0, st, reinterpret_cast<const unsigned char*>(a),

@@ -328,19 +328,11 @@ __global__ __launch_bounds__(256) void ns_gram_sum_kernel(const float* __restric
 // X' = c_lo lo + c_hi hi + c_prod (B + s I) hi, as hi' + lo', or, in the last step, rounded to bf16
 // into `out` in G's own layout.
 template <class S, bool LAST>
-__global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) void ns_update_kernel(
+__device__ __forceinline__ void ns_update_tile(
     const _Float16* __restrict__ bmat, const _Float16* __restrict__ hi, _Float16* lo,
     _Float16* __restrict__ hi_out, uint16_t* __restrict__ out, int m, int mp, int n, int ld,
-    int n_mtiles, int n_ctiles, int total, float c_prod, float c_hi, float c_lo, float c_out, int tall) {
-  static_assert(S::FN % 2 == 0, "sub-tiles in pairs");
-  __shared__ __attribute__((aligned(16))) unsigned char smem[S::kLdsBytes];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int per = n_mtiles * n_ctiles;
-  const int v = xcd_tile(blockIdx.x, total);
-  if (v < 0) return;
-  const int mat = v / per, t = v % per;
-  const int row0 = t % n_mtiles * S::BM, col0 = t / n_mtiles * S::BN;
+    float c_prod, float c_hi, float c_lo, float c_out, int tall, int mat, int row0, int col0,
+    unsigned char* smem, int wave, int lane) {
   const int64_t x0 = (int64_t)mat * m * ld;
   OperandLoader<S::BM, S::kWaves, false, S::KT> la;
   OperandLoader<S::BN, S::kWaves, true, S::KT> lb;
@@ -414,6 +406,33 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
       });
 }
 
+template <class S, bool LAST>
+__global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) void ns_update_kernel(
+    const _Float16* __restrict__ bmat, const _Float16* __restrict__ hi, _Float16* lo,
+    _Float16* __restrict__ hi_out, uint16_t* __restrict__ out, int m, int mp, int n, int ld,
+    int n_mtiles, int n_ctiles, int total, float c_prod, float c_hi, float c_lo, float c_out,
+    int tall) {
+  __shared__ __attribute__((aligned(16))) unsigned char smem[S::kLdsBytes];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int half;
+  const int v = xcd_tile_halves<S>(blockIdx.x, total, half);
+  if (v < 0) return;
+  const int mat = v / (n_mtiles * n_ctiles), t = v % (n_mtiles * n_ctiles);
+  const int row0 = t % n_mtiles * S::BM, col0 = t / n_mtiles * S::BN;
+  if constexpr (kHalves<S>) {
+    if (half >= 0) {
+      const int c = col0 + half * (S::BN / 2);
+      if (c < ld)
+        ns_update_tile<HalfTile<S>, LAST>(bmat, hi, lo, hi_out, out, m, mp, n, ld, c_prod, c_hi, c_lo,
+                                          c_out, tall, mat, row0, c, smem, wave, lane);
+      return;
+    }
+  }
+  ns_update_tile<S, LAST>(bmat, hi, lo, hi_out, out, m, mp, n, ld, c_prod, c_hi, c_lo, c_out, tall,
+                          mat, row0, col0, smem, wave, lane);
+}
+
 // ---- host side -----------------------------------------------------------------------------------
 using NsTile256 = TileShape<256, 256, 2, 4, 2, 2>;
 using NsTile128 = TileShape<128, 128, 2, 2, 2, 2>;
@@ -474,7 +493,7 @@ NsLayout ns_layout(int64_t n_mats, int rows, int cols) {
 
 bool ns_grid_fits(int64_t n_mats, int rows, int cols) {
   const int64_t mt = ceil_div(std::min(rows, cols), 64), ct = ceil_div(std::max(rows, cols), 64);
-  return n_mats <= 65535 && n_mats * mt * std::max(ct, (mt + 1) / 2) < (int64_t(1) << 31) - 8;
+  return n_mats <= 65535 && n_mats * mt * std::max(ct, (mt + 1) / 2) < (int64_t(1) << 31) - 256;
 }
 
 hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n_mats, int rows,
@@ -535,7 +554,7 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
         // weak directions, or (B + s I) lo, which vanishes in converged ones; only the last step's
         // error is not amplified in the weak ones
         constexpr bool kLast = decltype(last)::value;
-        hipLaunchKernelGGL((ns_update_kernel<S, kLast>), xcd_grid(update_tiles(S::BM)),
+        hipLaunchKernelGGL((ns_update_kernel<S, kLast>), xcd_grid_halves<S>(update_tiles(S::BM)),
                            dim3(S::kThreads), 0, st, poly, hi[0], lo, hi[1], out, L.m, L.mp, L.n,
                            L.ld, mt, ct, (int)update_tiles(S::BM), 1.f / kGramScale, a - ident, kLast ? a - ident : a,
                            1.f / sx, L.tall);
