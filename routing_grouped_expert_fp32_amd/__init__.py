@@ -514,6 +514,8 @@ def orthogonalise(g, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: floa
     _check_tensor("g", g, g.shape, torch.bfloat16, torch.float32)
     if out is not None:
         _check_tensor("out", out, g.shape, torch.bfloat16)
+    if len(coeffs) != 3:
+        raise ValueError("coeffs: expected (a, b, c)")
     abc = (ctypes.c_float * 3)(*[float(c) for c in coeffs])
     ctx, st = _on(_device_of(g, out, workspace), stream)
     with ctx:

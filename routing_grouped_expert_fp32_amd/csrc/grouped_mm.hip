@@ -38,6 +38,12 @@ __device__ __forceinline__ void expert_rows(const int32_t* __restrict__ off, int
   end = clamped(off[e + 1], begin, R);
 }
 
+// Blocks of BM rows that n rows make (unsigned: n + BM may pass 2^31).
+template <int BM>
+__device__ __forceinline__ int blocks_of(int n) {
+  return (int)(((unsigned)n + (BM - 1)) / BM);
+}
+
 // Blocks of BM rows of all experts in expert order: `total` of them; find(b) gives block b. Lane l
 // counts the blocks of experts [l * per, (l + 1) * per); a wave scan orders the lanes.
 template <int BM>
@@ -57,7 +63,7 @@ struct BlockScan {
       if (e < E) {
         int a, z;
         expert_rows(off, e, R, a, z);
-        c += (z - a + BM - 1) / BM;
+        c += blocks_of<BM>(z - a);
       }
     }
     int incl = c;
@@ -81,7 +87,7 @@ struct BlockScan {
       if (e >= E) break;
       int a, z;
       expert_rows(off, e, R, a, z);
-      const int n = (z - a + BM - 1) / BM;
+      const int n = blocks_of<BM>(z - a);
       if (left < n) {
         r = RowBlock{e, a + left * BM, min(BM, z - a - left * BM), left, n};
         break;
@@ -277,13 +283,18 @@ static void with_rows_tile(int64_t R, int64_t E, int64_t No, F&& f) {
 // Blocks that R rows of E experts can make.
 static int64_t max_blocks(int64_t R, int64_t E, int64_t bm) { return R / bm + std::min(R, E) + 1; }
 
+// A launch counts its threads in 32 bits.
+template <class S>
+static bool threads_fit(int64_t tiles) {
+  return (tiles + 8 * kXcdCus) * S::kThreads < (int64_t(1) << 32);
+}
+
 bool grouped_grid_fits(int64_t R, int64_t E, int64_t N, int64_t K) {
-  const int64_t lim = (int64_t(1) << 31) - 8;
-  bool ok = E * (ceil_div(N, 128) + 7) * (ceil_div(K, 128) + 7) < lim;
+  bool ok = threads_fit<Tile256>(E * (ceil_div(N, 128) + 7) * (ceil_div(K, 128) + 7));
   for (int64_t width : {N, K})
     with_rows_tile(R, E, width, [&](auto s) {
       using S = decltype(s);
-      ok = ok && max_blocks(R, E, S::BM) * ceil_div(width, S::BN) < lim - 8 * kXcdCus;
+      ok = ok && threads_fit<S>(max_blocks(R, E, S::BM) * ceil_div(width, S::BN));
     });
   return ok;
 }

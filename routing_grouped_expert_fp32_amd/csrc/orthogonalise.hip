@@ -20,7 +20,7 @@
 
 namespace beam {
 
-constexpr int kNormParts = 512;         // partial sums of squares of a matrix
+constexpr int kNormParts = 512;         // most partial sums of squares of a matrix
 constexpr float kGramScale = 256.f;     // A and B hold 2^8 times their values
 
 // X holds 2^k times its values, 2^k about sqrt(longer side): a matrix of orthonormal rows has entries
@@ -89,7 +89,7 @@ __global__ __launch_bounds__(256) void ns_norm_kernel(const void* __restrict__ g
 // 64 x 64 tiles through LDS.
 __global__ __launch_bounds__(256) void ns_init_kernel(const void* __restrict__ g, int g_bf16,
                                                       int rows, int cols, int tall, int m, int ld,
-                                                      const double* __restrict__ parts,
+                                                      const double* __restrict__ parts, int n_parts,
                                                       float scale, float eps,
                                                       _Float16* __restrict__ hi,
                                                       _Float16* __restrict__ lo) {
@@ -98,7 +98,8 @@ __global__ __launch_bounds__(256) void ns_init_kernel(const void* __restrict__ g
   const int64_t mat = blockIdx.z;
   double s = 0.0;
 #pragma unroll
-  for (int p = 0; p < kNormParts / 64; ++p) s += parts[mat * kNormParts + 64 * p + lane];
+  for (int p = 0; p < kNormParts / 64; ++p)
+    if (64 * p + lane < n_parts) s += parts[mat * n_parts + 64 * p + lane];
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
   const double den = sqrt(s) + (double)eps;
@@ -346,6 +347,51 @@ __device__ __forceinline__ void ns_update_tile(
   floatx4 acc[S::FM][S::FN];
   tile_zero<S>(acc);
   tile_kloop<S, false, true, true, S::FM>(la, lb, m, smem, wave, lane, acc);
+  if constexpr (LAST) {
+    if (tall) {   // G's rows are X's columns: as the accumulators lie, 4 x 4 transposed between lanes
+      const int r0 = row0 + (lane & 15), c0 = col0 + 16 * (wave % S::WN * S::FN) + 4 * (lane >> 4);
+      f16x4 h[S::FM][S::FN], l[S::FM][S::FN];
+      auto fetch = [&](int i) {   // clamped into the matrix; outside, the result is not stored
+        const int r = min(r0 + 16 * S::row_tile(wave / S::WN, i), m - 1);
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j) {
+          const int64_t at = x0 + (int64_t)r * ld + min(c0 + 16 * j, ld - 4);
+          h[i][j] = *reinterpret_cast<const f16x4*>(hi + at);
+          l[i][j] = *reinterpret_cast<const f16x4*>(lo + at);
+        }
+      };
+      uint16_t* o = out + (int64_t)mat * m * n;
+      constexpr int kAhead = S::FM < 2 ? S::FM : 2;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) fetch(i);
+#pragma unroll
+      for (int i = 0; i < S::FM; ++i) {
+        if (i + kAhead < S::FM) fetch(i + kAhead);
+        const int r = r0 + 16 * S::row_tile(wave / S::WN, i) - (lane & 3);
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j) {
+          floatx4 v;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            v[q] = c_out * (c_prod * acc[i][j][q] + c_hi * (float)h[i][j][q] +
+                            c_lo * (float)l[i][j][q]);
+          // row c + lane % 4 of G's layout, columns r .. r + 3
+          const u32x2 t = quad_transpose(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w), lane);
+          const int c = c0 + 16 * j + (lane & 3);
+          if (c >= n || r >= m) continue;
+          const int64_t at = (int64_t)c * m + r;
+          if ((m & 3) == 0) {
+            *reinterpret_cast<u32x2*>(o + at) = t;
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (r + q < m) o[at + q] = (uint16_t)(t[q >> 1] >> (16 * (q & 1)));
+          }
+        }
+      }
+      return;
+    }
+  }
   // in row order, four values a lane; hi and lo of the next two sub-tiles' rows are under way while
   // one's are used
   constexpr int kChunks = S::FN * 4, kRows = 64 / kChunks, kParts = 16 / kRows;
@@ -391,7 +437,7 @@ __device__ __forceinline__ void ns_update_tile(
           for (int q = 0; q < 4; ++q) nl[q] = (_Float16)(v[q] - (float)nh[q]);
           *reinterpret_cast<f16x4*>(hi_out + at) = nh;
           *reinterpret_cast<f16x4*>(lo + at) = nl;
-        } else if (!tall && (n & 3) == 0) {   // 8-byte aligned rows, four columns in or out
+        } else if ((n & 3) == 0) {   // 8-byte aligned rows, four columns in or out
           if (c < n)
             *reinterpret_cast<u32x2*>(out + ((int64_t)mat * m + r) * n + c) =
                 u32x2{pack_bf16(c_out * v.x, c_out * v.y), pack_bf16(c_out * v.z, c_out * v.w)};
@@ -399,9 +445,7 @@ __device__ __forceinline__ void ns_update_tile(
           uint16_t* o = out + (int64_t)mat * m * n;
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            if (c + q < n)
-              o[tall ? (int64_t)(c + q) * m + r : (int64_t)r * n + c + q] =
-                  (uint16_t)pack_bf16(c_out * v[q], 0.f);
+            if (c + q < n) o[(int64_t)r * n + c + q] = (uint16_t)pack_bf16(c_out * v[q], 0.f);
         }
       });
 }
@@ -492,8 +536,11 @@ NsLayout ns_layout(int64_t n_mats, int rows, int cols) {
 }
 
 bool ns_grid_fits(int64_t n_mats, int rows, int cols) {
+  // 64 x 64 tiles of 128 threads; wider ones have fewer of both together. A launch counts its threads
+  // in 32 bits.
   const int64_t mt = ceil_div(std::min(rows, cols), 64), ct = ceil_div(std::max(rows, cols), 64);
-  return n_mats <= 65535 && n_mats * mt * std::max(ct, (mt + 1) / 2) < (int64_t(1) << 31) - 256;
+  return n_mats <= 65535 &&
+         (n_mats * mt * std::max(ct, (mt + 1) / 2) + 8 * kXcdCus) * 512 < (int64_t(1) << 32);
 }
 
 hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n_mats, int rows,
@@ -509,11 +556,14 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
   const float a = coeffs[0], b = coeffs[1], c = coeffs[2];
   const float sx = x_scale(L.n);
   const float ident = std::round(-(b + c) * 4.f) / 4.f;   // exact in fp16 at the stored scale
-  hipLaunchKernelGGL(ns_norm_kernel, dim3(kNormParts, n_mats), dim3(256), 0, st, g, g_bf16,
-                     (int64_t)rows * cols, norm_parts);
+  const int64_t count = (int64_t)rows * cols;
+  const int n_parts = (int)std::min<int64_t>(kNormParts, ceil_div(count, 8192));
+  hipLaunchKernelGGL(ns_norm_kernel, dim3(n_parts, n_mats), dim3(256), 0, st, g, g_bf16, count,
+                     norm_parts);
   hipLaunchKernelGGL(ns_init_kernel,
                      dim3((unsigned)ceil_div(L.ld, 64), (unsigned)ceil_div(L.m, 64), n_mats),
-                     dim3(256), 0, st, g, g_bf16, rows, cols, L.tall, L.m, L.ld, norm_parts, sx, eps,
+                     dim3(256), 0, st, g, g_bf16, rows, cols, L.tall, L.m, L.ld, norm_parts,
+                     n_parts, sx, eps,
                      hi[0], lo);
   const int parts = gram_parts(n_mats, L.m, L.n);
   auto gram_tiles = [&](int side) { return n_mats * triangle(ceil_div(L.m, side)); };

@@ -83,6 +83,8 @@ def test_orthogonalise_refusals():
     assert _ns(dt=bm.BEAM_FP8_E4M3) == DTYPE
     assert _ns(steps=65) == UNSUPPORTED and _ns(rows=65537) == UNSUPPORTED
     assert _ns(n=65536) == UNSUPPORTED and _ns(n=60000, rows=65536, cols=65536) == UNSUPPORTED
+    assert _ns(n=9, rows=65536, cols=65536) == UNSUPPORTED   # a launch's threads are counted in 32 bits
+    assert _ns(n=1, rows=65536, cols=65536, nb=0) == WORKSPACE
     assert _ns(coeffs=None) == NULL and _ns(g=None) == NULL and _ns(out=None) == NULL
     assert _ns(ws=None) == NULL and _ns(n=0) == OK
     assert _ns(g=A[5] + 2) == ALIGN and _ns(out=A[5] + 8) == ALIGN and _ns(ws=A[5] + 1) == ALIGN
@@ -131,3 +133,5 @@ def test_binding_refuses_mismatched_tensors():
         bm.orthogonalise(torch.zeros(4))
     with pytest.raises(ValueError):
         bm.orthogonalise(torch.zeros(4, 4).half())
+    with pytest.raises(ValueError):
+        bm.orthogonalise(torch.zeros(4, 4), coeffs=(1.5, -0.5))
