@@ -23,8 +23,8 @@ namespace beam {
 // A block of rows of one expert, as found from the offsets.
 struct RowBlock {
   int e;          // expert
-  int row0;       // first row of the block
-  int rows;       // rows in the block
+  int row0;       // first row of the block (from find(): of the expert)
+  int rows;       // rows in the block (from find(): of the expert)
   int in_expert;  // the block's index among the expert's blocks
   int n_blocks;   // the expert's blocks
 };
@@ -44,7 +44,18 @@ __device__ __forceinline__ int blocks_of(int n) {
   return (int)(((unsigned)n + (BM - 1)) / BM);
 }
 
-// Blocks of BM rows of all experts in expert order: `total` of them; find(b) gives block b. Lane l
+// An expert's n rows in blocks_of(n) blocks of about the same height, counted in units of 64 rows (what
+// a tile's bodies tell apart): 655 rows as 256 + 256 + 143 cost less than as 320 + 320 + 15, whose
+// last block would read all the weights for one body's work.
+template <int BM>
+__device__ __forceinline__ void block_rows(int n, int n_blocks, int i, int& first, int& rows) {
+  constexpr int kUnit = BM % 64 == 0 ? 64 : BM;
+  const int units = blocks_of<kUnit>(n), each = units / n_blocks, more = units % n_blocks;
+  first = kUnit * (i * each + min(i, more));
+  rows = min(kUnit * (each + (i < more ? 1 : 0)), n - first);
+}
+
+// Blocks of at most BM rows of all experts in expert order: `total` of them; find(b) gives block b. Lane l
 // counts the blocks of experts [l * per, (l + 1) * per); a wave scan orders the lanes.
 template <int BM>
 struct BlockScan {
@@ -89,7 +100,7 @@ struct BlockScan {
       expert_rows(off, e, R, a, z);
       const int n = blocks_of<BM>(z - a);
       if (left < n) {
-        r = RowBlock{e, a + left * BM, min(BM, z - a - left * BM), left, n};
+        r = RowBlock{e, a, z - a, left, n};
         break;
       }
       left -= n;
@@ -177,10 +188,10 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
     const int sz = min(kTileGroup, blk.n_blocks - g0);
     const int at = v - (v / n_ctiles - (blk.in_expert - g0)) * n_ctiles;   // tile within the group
     ctile = at / sz;
-    int lo, hi;
-    expert_rows(offsets, blk.e, R, lo, hi);
-    blk.row0 = lo + (g0 + at % sz) * S::BM;
-    blk.rows = min(S::BM, hi - blk.row0);
+    int first, rows;
+    block_rows<S::BM>(blk.rows, blk.n_blocks, g0 + at % sz, first, rows);
+    blk.row0 += first;
+    blk.rows = rows;
   }
   const int col0 = ctile * S::BN;
   if constexpr (kHalves<S>) {
