@@ -269,7 +269,8 @@ BEAM_API beam_status_t beam_moe_forward_boundary(
  *   and x may then both be NULL).
  * The products are exact and summed in FP32 on the matrix cores, in an order that depends on the
  * sizes alone: equal calls give equal bits.
- * Limits: N % 8 == 0, K % 8 == 0, N and K <= 2^20, N * K < 2^31, E <= 4096, R < 2^31. No workspace. */
+ * Limits: N % 8 == 0, K % 8 == 0, N and K <= 2^20, N * K < 2^31, E <= 4096, R < 2^31, and a launch of
+ * fewer than 2^32 threads (BEAM_ERR_UNSUPPORTED otherwise; at N = K = 5120 R < 2^30). No workspace. */
 BEAM_API beam_status_t beam_moe_grouped_mm(const void* x, const void* w, const int32_t* offsets,
                                            void* out, int64_t R, int32_t E, int32_t N, int32_t K,
                                            int32_t out_dtype, void* stream);
@@ -315,7 +316,8 @@ BEAM_API size_t beam_residual_boundary_backward_workspace_bytes(int64_t T, int32
  * sums: before its last rounding to bf16 the result is within about 0.2% (2-norm) of the exact
  * iteration's for coefficients that keep the singular values near 1. Iterates that grow past fp16
  * (entries beyond 65504 / (2 sqrt(longer side))) come out infinite or NaN.
- * Limits: rows and cols <= 65536, n_mats <= 65535, steps <= 64. Equal calls give equal bits. */
+ * Limits: rows and cols <= 65536, n_mats <= 65535, steps <= 64, and a launch of fewer than 2^32 threads.
+ * Equal calls give equal bits. */
 BEAM_API beam_status_t beam_moe_orthogonalise(const void* g, int32_t g_dtype, void* out,
                                               int64_t n_mats, int32_t rows, int32_t cols,
                                               int32_t steps, const float* coeffs, float eps,
