@@ -270,7 +270,8 @@ BEAM_API beam_status_t beam_moe_forward_boundary(
  * The products are exact and summed in FP32 on the matrix cores, in an order that depends on the
  * sizes alone: equal calls give equal bits.
  * Limits: N % 8 == 0, K % 8 == 0, N and K <= 2^20, N * K < 2^31, E <= 4096, R < 2^31, and a launch of
- * fewer than 2^32 threads (BEAM_ERR_UNSUPPORTED otherwise; at N = K = 5120 R < 2^30). No workspace. */
+ * fewer than 2^32 threads (BEAM_ERR_UNSUPPORTED otherwise; at N = K = 5120 about 10^8 rows). No
+ * workspace. */
 BEAM_API beam_status_t beam_moe_grouped_mm(const void* x, const void* w, const int32_t* offsets,
                                            void* out, int64_t R, int32_t E, int32_t N, int32_t K,
                                            int32_t out_dtype, void* stream);

@@ -477,6 +477,188 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
                           mat, row0, col0, smem, wave, lane);
 }
 
+// Small matrices (shorter side <= 64, longer <= 512): all steps in one launch, a workgroup a matrix.
+// X stays in registers in 32 bits (wave w holds column tiles w, w + 8, ...), its fp16 half for the
+// products in LDS, where the two 64 x 64 matrices lie too; each wave computes two of their 16
+// sub-tiles. The formats and scales are those above, with X itself in lo's place. Bound by latency: one
+// 64 x 512 matrix, five steps, 30 us (80 in a launch a product), 2000 of them 292 us.
+constexpr int kSmallM = 64, kSmallN = 512, kSmallWaves = 8;
+constexpr int kSmallPitch = 2 * kSmallN + 16, kSquarePitch = 2 * kSmallM + 16;   // bytes
+constexpr int kSmallTiles = kSmallN / 16 / kSmallWaves;   // column tiles a wave
+
+struct NsSmallArgs {
+  const void* g;
+  uint16_t* out;
+  int g_bf16, tall, m, n, steps;
+  float a, b, c, ident, eps, scale;
+};
+
+__global__ __launch_bounds__(64 * kSmallWaves) void ns_small_kernel(NsSmallArgs p) {
+  __shared__ __attribute__((aligned(16))) unsigned char
+      smem[kSmallM * kSmallPitch + 2 * kSmallM * kSquarePitch + 8 * kSmallWaves];
+  unsigned char* const xs = smem;
+  unsigned char* const as = xs + kSmallM * kSmallPitch;
+  unsigned char* const bs = as + kSmallM * kSquarePitch;
+  double* const red = reinterpret_cast<double*>(bs + kSmallM * kSquarePitch);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r15 = lane & 15, g = lane >> 4;
+  const int m = p.m, n = p.n;
+  const int64_t base = (int64_t)blockIdx.x * m * n;
+  const int tiles = (n + 31) / 32 * 2;   // 16-column tiles, whole steps of 32
+  auto col_tile = [&](int j) { return j * kSmallWaves + wave; };
+
+  // x[i][j]: rows 16 i + lane % 16, columns 16 col_tile(j) + 4 (lane / 16) + 0..3
+  floatx4 x[4][kSmallTiles];
+  double s = 0.0;
+  const bool by4 = !p.tall && (n & 3) == 0;   // then four columns are all in or all out, and aligned
+#pragma unroll
+  for (int j = 0; j < kSmallTiles; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 16 * i + r15, c = 16 * col_tile(j) + 4 * g;
+      x[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+      if (r >= m || c >= n) continue;
+      if (by4) {
+        const int64_t at = base + (int64_t)r * n + c;
+        if (p.g_bf16) {
+          const u32x2 v = *reinterpret_cast<const u32x2*>(reinterpret_cast<const uint16_t*>(p.g) + at);
+          x[i][j] = floatx4{bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+        } else {
+          x[i][j] = *reinterpret_cast<const floatx4*>(reinterpret_cast<const float*>(p.g) + at);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (c + q < n)
+            x[i][j][q] =
+                load_as_f32(p.g, base + (p.tall ? (int64_t)(c + q) * m + r : (int64_t)r * n + c + q),
+                            p.g_bf16);
+      }
+    }
+#pragma unroll
+  for (int j = 0; j < kSmallTiles; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s += (double)x[i][j][q] * x[i][j][q];
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
+  if (lane == 0) red[wave] = s;
+  __syncthreads();
+  s = 0.0;
+#pragma unroll
+  for (int w = 0; w < kSmallWaves; ++w) s += red[w];
+  const double den = sqrt(s) + (double)p.eps;
+  const double mul = den > 0.0 ? (double)p.scale / den : 0.0;   // a zero matrix stays zero
+#pragma unroll
+  for (int j = 0; j < kSmallTiles; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[i][j][q] = (float)(x[i][j][q] * mul);
+
+  const int r = 16 * (wave >> 1) + r15;   // the wave's sub-tiles of A and B: two of a row
+  auto frag = [&](const unsigned char* at) { return *reinterpret_cast<const intx4*>(at); };
+  for (int step = 0; step < p.steps; ++step) {
+#pragma unroll
+    for (int j = 0; j < kSmallTiles; ++j)
+      if (col_tile(j) < tiles)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<u32x2*>(xs + (16 * i + r15) * kSmallPitch + 32 * col_tile(j) + 8 * g) =
+              u32x2{pack_f16(x[i][j].x, x[i][j].y), pack_f16(x[i][j].z, x[i][j].w)};
+    __syncthreads();
+    // A
+    floatx4 d[2] = {};
+#pragma unroll 2
+    for (int k = 0; k < tiles / 2; ++k) {
+      const intx4 fa = frag(xs + r * kSmallPitch + 64 * k + 16 * g);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        d[t] = tile_mma<true>(
+            frag(xs + (16 * (2 * (wave & 1) + t) + r15) * kSmallPitch + 64 * k + 16 * g), fa, d[t]);
+    }
+    const float c0 = kGramScale / (p.scale * p.scale);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int c = 16 * (2 * (wave & 1) + t) + 4 * g;
+      *reinterpret_cast<u32x2*>(as + r * kSquarePitch + 2 * c) =
+          u32x2{pack_f16(d[t].x * c0, d[t].y * c0), pack_f16(d[t].z * c0, d[t].w * c0)};
+    }
+    __syncthreads();
+    // B + s I
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int c = 16 * (2 * (wave & 1) + t) + 4 * g;
+      floatx4 e = {};
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        e = tile_mma<true>(
+            frag(as + (16 * (2 * (wave & 1) + t) + r15) * kSquarePitch + 64 * k + 16 * g),
+            frag(as + r * kSquarePitch + 64 * k + 16 * g), e);
+      const f16x4 a = *reinterpret_cast<const f16x4*>(as + r * kSquarePitch + 2 * c);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        e[q] =
+            p.c / kGramScale * e[q] + p.b * (float)a[q] + (r == c + q ? p.ident * kGramScale : 0.f);
+      *reinterpret_cast<u32x2*>(bs + r * kSquarePitch + 2 * c) =
+          u32x2{pack_f16(e.x, e.y), pack_f16(e.z, e.w)};
+    }
+    __syncthreads();
+    // X
+    const bool last = step + 1 == p.steps;
+#pragma unroll
+    for (int j = 0; j < kSmallTiles; ++j) {
+      if (col_tile(j) >= tiles) continue;
+      floatx4 u[4] = {};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        // columns across the contraction: transposing reads of rows 32 k + 8 g + 0..3 and 4..7
+        const unsigned char* at = xs + (32 * k + 8 * g + (r15 >> 2)) * kSmallPitch +
+                                  32 * col_tile(j) + 8 * (r15 & 3);
+        const u32x2 lo = __builtin_bit_cast(
+            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at));
+        const u32x2 hi = __builtin_bit_cast(
+            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 4 * kSmallPitch)));
+        const intx4 fx{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          u[i] = tile_mma<true>(fx, frag(bs + (16 * i + r15) * kSquarePitch + 64 * k + 16 * g), u[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float v = x[i][j][q], h = (float)(_Float16)v;
+          // a X - s hi + (B + s I) hi, or, in the last step, (a - s) X + (B + s I) hi
+          x[i][j][q] = u[i][q] * (1.f / kGramScale) + p.a * v - p.ident * (last ? v : h);
+        }
+    }
+  }
+  const float back = 1.f / p.scale;
+#pragma unroll
+  for (int j = 0; j < kSmallTiles; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int ro = 16 * i + r15, co = 16 * col_tile(j) + 4 * g;
+      if (ro >= m || co >= n) continue;
+      const floatx4 v = x[i][j] * back;
+      if (by4) {
+        *reinterpret_cast<u32x2*>(p.out + base + (int64_t)ro * n + co) =
+            u32x2{pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)};
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (co + q < n)
+            p.out[base + (p.tall ? (int64_t)(co + q) * m + ro : (int64_t)ro * n + co + q)] =
+                (uint16_t)pack_bf16(v[q], 0.f);
+      }
+    }
+}
+
+static bool ns_is_small(int m, int n) { return m <= kSmallM && n <= kSmallN; }
+
 // ---- host side -----------------------------------------------------------------------------------
 using NsTile256 = TileShape<256, 256, 2, 4, 2, 2>;
 using NsTile128 = TileShape<128, 128, 2, 2, 2, 2>;
@@ -489,12 +671,12 @@ static int64_t triangle(int64_t n) { return n * (n + 1) / 2; }
 // The largest tile whose workgroups fill the GPU (256 x 256 ones from three quarters on: they multiply
 // a quarter faster); `count` is their number for a tile side. 2560 x 5120, us, 256 / 128 wide tiles:
 // A of 1, 2, 4, 8 matrices 123 / 58, 120 / 81, 134 / 153, 268 / 301; the update of 1, 8: 83 / 94,
-// 628 / 709.
+// 628 / 709. No tile is twice as high as the m rows there are.
 template <class Count, class F>
-static void with_ns_tile(Count&& count, F&& f) {
-  if (count(256) >= kNsCus * 3 / 4)
+static void with_ns_tile(int m, Count&& count, F&& f) {
+  if (m > 128 && count(256) >= kNsCus * 3 / 4)
     f(NsTile256{});
-  else if (count(128) >= kNsCus)
+  else if (m > 64 && count(128) >= kNsCus)
     f(NsTile128{});
   else
     f(NsTile64{});
@@ -515,6 +697,10 @@ NsLayout ns_layout(int64_t n_mats, int rows, int cols) {
   L.n = std::max(rows, cols);
   L.mp = (L.m + 7) / 8 * 8;
   L.ld = (L.n + 7) / 8 * 8;
+  if (ns_is_small(L.m, L.n)) {   // uses none
+    L.total = 16;
+    return L;
+  }
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -556,6 +742,11 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
   const float a = coeffs[0], b = coeffs[1], c = coeffs[2];
   const float sx = x_scale(L.n);
   const float ident = std::round(-(b + c) * 4.f) / 4.f;   // exact in fp16 at the stored scale
+  if (ns_is_small(L.m, L.n)) {
+    hipLaunchKernelGGL(ns_small_kernel, dim3(n_mats), dim3(64 * kSmallWaves), 0, st,
+                       NsSmallArgs{g, out, g_bf16, L.tall, L.m, L.n, steps, a, b, c, ident, eps, sx});
+    return hipGetLastError();
+  }
   const int64_t count = (int64_t)rows * cols;
   const int n_parts = (int)std::min<int64_t>(kNormParts, ceil_div(count, 8192));
   hipLaunchKernelGGL(ns_norm_kernel, dim3(n_parts, n_mats), dim3(256), 0, st, g, g_bf16, count,
@@ -580,7 +771,7 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
       hipLaunchKernelGGL((ns_gram_sum_kernel<S>), dim3((unsigned)(n_mats * per * 4)), dim3(256), 0,
                          st, sums, gram, L.m, L.mp, per, used, c0);
     } else {
-      with_ns_tile(gram_tiles, [&](auto tile) {
+      with_ns_tile(L.m, gram_tiles, [&](auto tile) {
         using S = decltype(tile);
         hipLaunchKernelGGL((ns_gram_kernel<S, false>), xcd_grid(gram_tiles(S::BM)),
                            dim3(S::kThreads), 0, st, hi[0], gram, L.m, L.mp, L.ld, L.n,
@@ -588,7 +779,7 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
                            0.f);
       });
     }
-    with_ns_tile(gram_tiles, [&](auto tile) {
+    with_ns_tile(L.m, gram_tiles, [&](auto tile) {
       using S = decltype(tile);
       hipLaunchKernelGGL((ns_gram_kernel<S, true>), xcd_grid(gram_tiles(S::BM)),
                          dim3(S::kThreads), 0, st, gram, poly, L.m, L.mp, L.mp, L.m,
@@ -596,7 +787,7 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
                          ident * kGramScale);
     });
     auto update_tiles = [&](int side) { return n_mats * ceil_div(L.m, side) * ceil_div(L.ld, side); };
-    with_ns_tile(update_tiles, [&](auto tile) {
+    with_ns_tile(L.m, update_tiles, [&](auto tile) {
       using S = decltype(tile);
       const int mt = (int)ceil_div(L.m, S::BM), ct = (int)ceil_div(L.ld, S::BN);
       auto update = [&](auto last) {

@@ -25,7 +25,6 @@ def _check(g, out, steps=5, coeffs=MUON, eps=1e-7):
         want = training.orthogonalise(m, steps, coeffs, eps)
         norm = np.linalg.norm(want)
         d = np.abs(o - want)
-        print("  rel", np.linalg.norm(d) / norm if norm else d.max(), flush=True)
         assert np.linalg.norm(d) <= TOL * norm
         rms = norm / np.sqrt(want.size)
         assert (d <= 16 * TOL * np.maximum(np.abs(want), rms)).all()
@@ -43,6 +42,16 @@ def _gauss(*shape, seed=0, dtype=torch.float32, scale=1.0):
 def test_against_oracle(shape, dtype):
     print("orthogonalise", shape, dtype, flush=True)
     g = _gauss(*shape, seed=sum(shape), dtype=dtype)
+    _check(g, bm.orthogonalise(g.cuda()))
+
+
+@pytest.mark.parametrize("shape", [(300, 20, 33), (64, 512), (512, 64), (63, 511), (64, 513),
+                                   (260, 70, 70), (260, 100, 66), (192, 130, 300), (192, 300, 130),
+                                   (200, 131, 137), (200, 137, 131)])
+def test_batches_of_every_tile(shape):
+    # one launch a batch up to 64 x 512; tiles of 64, 128 and 256, the last in column halves too
+    print("orthogonalise", shape, flush=True)
+    g = _gauss(*shape, seed=sum(shape), dtype=torch.bfloat16)
     _check(g, bm.orthogonalise(g.cuda()))
 
 
