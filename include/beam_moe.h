@@ -25,9 +25,9 @@
  *   - `stream` is a hipStream_t (NULL = the null stream). Every call is asynchronous on it; none
  *     allocates device memory, frees, or synchronises the host (except under BEAM_MOE_SYNC_CHECK).
  *   - Every argument is validated on the host before the first launch: a non-zero status means
- *     nothing was launched. T = 0 is a successful no-op. Device-side faults surface at the caller's
- *     next synchronisation. Unsupported shapes or dtypes return BEAM_ERR_UNSUPPORTED: there is no
- *     fallback path.
+ *     nothing was launched. T = 0 is a successful no-op (unless stated below). Device-side faults
+ *     surface at the caller's next synchronisation. Unsupported shapes or dtypes return
+ *     BEAM_ERR_UNSUPPORTED: there is no fallback path.
  *   - Calls on distinct workspaces may run concurrently on different streams; calls that share a
  *     workspace must be ordered by the caller.
  *   - Debugging: with the environment variable BEAM_MOE_SYNC_CHECK set to anything but "0" (read
@@ -293,7 +293,8 @@ BEAM_API beam_status_t beam_moe_grouped_mm_dw(const void* dy, const void* x, con
  *   d_h_out    [T][hidden] bf16: gradient of h_out; NULL: zero
  *   d_x_next   [T][hidden] bf16: gradient of x_next
  *   d_y        [T][hidden] y_dtype out;  d_h [T][hidden] bf16 out (may be d_h_out itself)
- *   d_gamma_post, d_gamma_next  [hidden] fp32 out, over this call's tokens (T = 0: not written)
+ *   d_gamma_post, d_gamma_next  [hidden] fp32 out, over this call's tokens (T = 0: set to zero;
+ *              the other pointers may then be NULL)
  *   gamma_post, gamma_next, depth_n, eps and the limits as for beam_residual_boundary
  *   workspace  device scratch of at least beam_residual_boundary_backward_workspace_bytes(T, hidden)
  * A row of zeros with eps = 0 gives NaN, as in the forward. Equal calls give equal bits. */

@@ -479,12 +479,10 @@ def residual_boundary_backward(y, h_out, gamma_post, gamma_next, d_h_out, d_x_ne
     with ctx:
         d_y = torch.empty_like(y) if d_y is None else d_y
         d_h = torch.empty_like(h_out) if d_h is None else d_h
-        # no tokens: the call writes nothing, and the sums over none are zero
-        new = torch.empty if T > 0 else torch.zeros
         if d_gamma_post is None:
-            d_gamma_post = new((H,), dtype=f32, device=y.device)
+            d_gamma_post = torch.empty((H,), dtype=f32, device=y.device)
         if d_gamma_next is None:
-            d_gamma_next = new((H,), dtype=f32, device=y.device)
+            d_gamma_next = torch.empty((H,), dtype=f32, device=y.device)
         if workspace is None:
             nbytes = residual_boundary_backward_workspace_bytes(T, H)
             workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=y.device)

@@ -114,9 +114,9 @@ beam_status_t beam_residual_boundary_backward(
   if (y_dtype != BEAM_F32 && y_dtype != BEAM_BF16) return BEAM_ERR_DTYPE;
   if (hidden % 256 != 0 || hidden > beam::boundary_max_hidden() || T >= (int64_t(1) << 31))
     return BEAM_ERR_UNSUPPORTED;
-  if (T == 0) return BEAM_OK;
-  if (!y || !h_out || !gamma_post || !gamma_next || !d_x_next || !d_y || !d_h || !d_gamma_post ||
-      !d_gamma_next || !workspace)
+  if (!d_gamma_post || !d_gamma_next) return BEAM_ERR_NULL;
+  // without tokens the weights' gradients are still written (zeros), and nothing else is touched
+  if (T > 0 && (!y || !h_out || !gamma_post || !gamma_next || !d_x_next || !d_y || !d_h || !workspace))
     return BEAM_ERR_NULL;
   const void* ptrs[] = {y,   h_out, gamma_post,   gamma_next,   d_h_out,  d_x_next,
                         d_y, d_h,   d_gamma_post, d_gamma_next, workspace};

@@ -202,6 +202,10 @@ int boundary_bwd_parts(int64_t T, int H) {
 
 hipError_t launch_boundary_bwd(const BoundaryBwdArgs& a, int64_t T, int H, hipStream_t st) {
   const int n_parts = boundary_bwd_parts(T, H);
+  auto reduce = [&]() {
+    hipLaunchKernelGGL(gamma_reduce_kernel, dim3(2 * H / 64), dim3(64 * kReduceRows), 0, st, a.parts,
+                       n_parts, a.d_gamma_post, a.d_gamma_next, H);
+  };
   auto go = [&](auto th_tag, auto ch_tag) {
     constexpr int TH = decltype(th_tag)::value, CH = decltype(ch_tag)::value;
     auto run = [&](auto yb, auto dh) {
@@ -216,6 +220,10 @@ hipError_t launch_boundary_bwd(const BoundaryBwdArgs& a, int64_t T, int H, hipSt
       a.d_h_in ? run(std::false_type{}, std::true_type{})
                : run(std::false_type{}, std::false_type{});
   };
+  if (n_parts == 0) {   // no tokens: the weights' gradients are sums over nothing
+    reduce();
+    return hipGetLastError();
+  }
   const int th = bwd_threads(H), need = (int)ceil_div(H, 4 * th);
   auto chunks = [&](auto th_tag) {
     if (need <= 1)
@@ -238,8 +246,7 @@ hipError_t launch_boundary_bwd(const BoundaryBwdArgs& a, int64_t T, int H, hipSt
   else   // need is 3 or 4
     need <= 3 ? go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 3>{})
               : go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
-  hipLaunchKernelGGL(gamma_reduce_kernel, dim3(2 * H / 64), dim3(64 * kReduceRows), 0, st, a.parts,
-                     n_parts, a.d_gamma_post, a.d_gamma_next, H);
+  reduce();
   return hipGetLastError();
 }
 

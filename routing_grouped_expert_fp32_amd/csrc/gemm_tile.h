@@ -371,6 +371,8 @@ __device__ __forceinline__ void tile_rows(unsigned char* smem, int wave, int lan
 #pragma unroll
     for (int j = 0; j < S::FN; ++j)
       put(i, j, buf + (lane & 15) * kPitch + (16 * j + 4 * (lane >> 4)) * kSize);
+    // the lanes read each other's values: the compiler keeps the order (no instruction)
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int p = 0; p < 16 / kRows; ++p) {
       const int r = p * kRows + lane / kLanes, c = lane % kLanes;

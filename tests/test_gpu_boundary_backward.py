@@ -91,6 +91,9 @@ def test_zero_rows_and_no_tokens():
     g = torch.ones(512, device="cuda")
     d_y, d_h, a, b = bm.residual_boundary_backward(e, e, g, g, e, e, 5, 1e-6)
     assert d_y.shape == d_h.shape == (0, 512) and not a.any() and not b.any()
+    a, b = torch.full((2, 512), 7.0, device="cuda")   # a buffer that is given is set to zero as well
+    bm.residual_boundary_backward(e, e, g, g, e, e, 5, 1e-6, d_gamma_post=a, d_gamma_next=b)
+    assert not a.any() and not b.any()
 
 
 def test_non_finite_token_stays_in_its_row():

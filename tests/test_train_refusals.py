@@ -52,7 +52,8 @@ def test_boundary_backward_refusals():
     assert _bwd(eps=-1.0) == SHAPE and _bwd(eps=float("nan")) == SHAPE
     assert _bwd(ydt=bm.BEAM_FP8_E4M3) == DTYPE
     assert _bwd(H=500) == UNSUPPORTED and _bwd(H=16640) == UNSUPPORTED and _bwd(T=1 << 31) == UNSUPPORTED
-    assert _bwd(T=0) == OK
+    assert _bwd(T=0, dgp=None) == NULL and _bwd(T=0, dgn=None) == NULL   # these are written
+    assert _bwd(T=0, dgn=A[8]) == ALIAS
     names = ["y", "h", "gp", "gn", "dx", "d_y", "d_h", "dgp", "dgn", "ws"]
     for k in names:
         assert _bwd(**{k: None}) == NULL, k
@@ -101,6 +102,8 @@ def test_valid_calls_without_gpu_report_device():
         assert _grouped(e) == DEVICE
     assert _grouped(ENTRIES[2], a=None, b=None, R=0) == DEVICE
     assert _bwd() == DEVICE and _bwd(dh=None) == DEVICE and _bwd(d_h=A[4]) == DEVICE
+    assert _bwd(T=0, y=None, h=None, gp=None, gn=None, dh=None, dx=None, d_y=None, d_h=None, ws=None,
+                nb=0) == DEVICE
     assert _ns() == DEVICE
 
 
