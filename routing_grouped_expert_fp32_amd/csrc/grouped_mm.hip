@@ -205,6 +205,34 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   grouped_rows_tile<S, WCOL, OUT_BF16>(a, w, out, blk, col0, No, Kc, smem, wave, lane);
 }
 
+// Expert at position `pos` < E of the order in which those with more than 1.5 times the mean's rows come
+// first, and its rows [begin, end).
+__device__ __forceinline__ int heavy_first(const int32_t* __restrict__ off, int E, int R, int pos,
+                                           int lane, int& begin, int& end) {
+  const int heavy_rows = R / E + R / E / 2;
+  int a0 = 0, z0 = 0;   // the first 64 experts' rows
+  if (lane < E) expert_rows(off, lane, R, a0, z0);
+#pragma unroll
+  for (int light = 0; light < 2; ++light)
+    for (int base = 0; base < E; base += 64) {
+      const bool in = base + lane < E;
+      int a = a0, z = z0;
+      if (base > 0 && in) expert_rows(off, base + lane, R, a, z);
+      const uint64_t mask = __ballot(in && (z - a > heavy_rows) != (bool)light);
+      const int n = __popcll(mask);
+      if (pos < n) {
+        const bool mine = mask >> lane & 1 && __popcll(mask & ((uint64_t(1) << lane) - 1)) == pos;
+        const int at = __ffsll((unsigned long long)__ballot(mine)) - 1;
+        begin = uniform(__shfl(a, at));
+        end = uniform(__shfl(z, at));
+        return uniform(base + at);
+      }
+      pos -= n;
+    }
+  begin = end = 0;
+  return -1;
+}
+
 // dw[e] (N x K) = dy_e^T x_e: both operands lie across the contraction (the expert's rows).
 //
 // Each expert's tiles are cut into 8 runs, one per XCD, so an expert with many rows loads all XCDs
@@ -219,15 +247,16 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int per = n_mtiles * n_ctiles, run = (per + 7) >> 3;
-  const int local = blockIdx.x >> 3, e = local / run;
+  const int local = blockIdx.x >> 3;
   const int t = (blockIdx.x & 7) * run + local % run;
-  if (e >= E || t >= per) return;
+  if (local / run >= E || t >= per) return;
+  int begin, end;
+  const int e = heavy_first(offsets, E, R, local / run, lane, begin, end);
+  if (e < 0) return;   // not reached: every expert has a position
   // tiles of one matrix in bands of kTileGroup tile rows, column by column
   const int m0 = t / (kTileGroup * n_ctiles) * kTileGroup;
   const int sz = min(kTileGroup, n_mtiles - m0), at = t - m0 * n_ctiles;
   const int row0 = (m0 + at % sz) * S::BM, col0 = at / sz * S::BN;
-  int begin, end;
-  expert_rows(offsets, e, R, begin, end);
   const int64_t a_ld = (int64_t)N * 2, b_ld = (int64_t)K * 2;
   OperandLoader<S::BM, S::kWaves, true, S::KT> la;
   OperandLoader<S::BN, S::kWaves, true, S::KT> lb;
