@@ -386,9 +386,9 @@ def _on(dev, stream):
     current one) current, so that results and workspaces allocated inside belong to the stream that
     uses them."""
     if stream is None:
-        if dev.index == torch.cuda.current_device():
-            return _NO_CONTEXT, torch.cuda.current_stream(dev).cuda_stream
-        return torch.cuda.device(dev), torch.cuda.current_stream(dev).cuda_stream
+        # torch.cuda.current_stream(dev).cuda_stream without the Stream object, 1.8 us of a call's 10
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)
+        return (_NO_CONTEXT if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)), handle
     if stream.device != dev:
         raise ValueError("the stream is on another device than the tensors")
     return torch.cuda.stream(stream), stream.cuda_stream

@@ -14,6 +14,7 @@
 // Workgroup L runs on XCD L % 8, so the tiles are cut into 8 contiguous runs, one per XCD, whose
 // neighbours share operands in that XCD's L2.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "gemm_tile.h"
@@ -270,54 +271,107 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
                                  (int64_t)K * kSize, N - row0, K - col0, smem, wave, lane);
 }
 
-// Tiles of the forward and the input gradient, by the mean number of rows of an expert (the counts
-// themselves are on the device). Measured at 32 experts of 5120 x 5120 (us, forward; reading the
-// 1.68 GB of weights alone takes about 260):
-//   rows / expert         1    64   110   156   219   256
-//   32 x 128  (4, 4)    173   443
-//   128 x 256 (2, 3)          308   324   433
-//   192 x 256 (2, 3)          311   323   350
-//   256 x 256 (2, 3)                      414   567
-//   320 x 256 (2, 2)          381   384   396   443   454
-// Few rows: narrow tiles, many workgroups streaming weights. More: one block an expert if it can be,
-// as every further block reads the weights again (counts spread by about the square root of their
-// mean: 2.5 of it are allowed for); the B operand's third stage covers their latency while LDS
-// lasts. Past 1536 rows blocks are many anyway and 256 x 256 multiplies fastest (one matrix of 8192
-// x 8192, 8192 rows: 790 us, 320 x 256 895). Where a tile leaves CUs without work, 64 x 64: 523
-// rows, 16 experts of 776 x 520, 6.9 us (128 x 128 tiles 12.3).
+// The tile of a call is the one that a model of its time puts first; the experts' own row counts are on
+// the device, so it goes by their mean. Per tile shape, in us (fitted to some 400 calls between one
+// row and 65536, one expert and 256, widths of 128 to 8192, each measured with every tile):
+struct TileCost {
+  double mb;      // a megabyte from or to HBM (small tiles keep more loads in flight)
+  double l2_mb;   // a megabyte of operands that other tiles read too
+  double ends;    // a tile's start and end
+  double stage;   // 64 values of its contraction
+  double alone;   // the same on a CU that runs no other tile
+};
+// Workgroups of a shape that the GPU holds at once (the LDS rings decide).
+constexpr int kGroupedCus = 256;
+template <class S>
+constexpr int kSlots = kGroupedCus * (160 * 1024 / S::kLdsBytes);
+
+// Calls f with the candidate for which us(candidate) is least.
+template <class Us, class F, class... S>
+static void with_least(Us&& us, F&& f, S... tiles) {
+  const double t[] = {us(tiles)...};
+  const int pick = (int)(std::min_element(t, t + sizeof...(S)) - t);
+  int i = 0;
+  ((i++ == pick ? f(tiles) : void()), ...);
+}
+
+// Forward and input gradient. Measured (us, forward, bf16; the last columns with few columns and
+// many rows, 40 experts of 632 x 1824 and 27 of 616 x 592):
+//                        32 experts of 5120 x 5120, rows each          467    322
+//                        64    110    156    219    256    375    656   rows   rows
+//    32 x 128  (4, 4)   449    572    882   1084   1283   1779   3067    106    24
+//    64 x 64   (3, 3)   420    516    652    788    969   1379   2286     91    21
+//   128 x 128  (2, 2)   338    360    462    526    631    771   1339     60    15
+//   128 x 256  (2, 3)   300    318    438    478    570    741   1263     67    16
+//   192 x 256  (2, 3)   307    312    339    494    551    687   1119     69    21
+//   256 x 256  (2, 3)   324    324    350    403    505    651   1050     57    17
+//   320 x 256  (2, 2)   374    362    380    408    451    676    995     55    19
+// Few rows: narrow tiles, many workgroups streaming weights. More: one block an expert if it can be, as
+// every further block reads the weights again (rows spread by about the square root of their mean:
+// 2.5 of it are allowed for); the B operand's third stage covers their latency while LDS lasts.
+// Taken by this rule, the calls it was fitted to take 7% more than each one's best tile.
 using TileStream = TileShape<32, 128, 1, 4, 4, 4>;
 using Tile64 = TileShape<64, 64, 1, 2, 3, 3>;
+using TilePair = TileShape<128, 128, 2, 2, 2, 2>;
 using Tile128 = TileShape<128, 256, 2, 4, 2, 3>;
 using Tile192 = TileShape<192, 256, 2, 4, 2, 3>;
 using Tile256Deep = TileShape<256, 256, 2, 4, 2, 3>;
-using Tile256 = TileShape<256, 256, 2, 4, 2, 2>;
 using Tile320 = TileShape<320, 256, 2, 4, 2, 2>;
-constexpr int kGroupedCus = 256;
+static constexpr TileCost rows_cost(TileStream) { return {.172, .1, 1.8, .41, 0.}; }
+static constexpr TileCost rows_cost(Tile64) { return {.228, .1, 2.3, .34, 0.}; }
+static constexpr TileCost rows_cost(TilePair) { return {.240, .1, 1.7, .82, 0.}; }
+static constexpr TileCost rows_cost(Tile128) { return {.215, .1, 3.2, .50, 0.}; }
+static constexpr TileCost rows_cost(Tile192) { return {.235, .1, 3.2, .59, 0.}; }
+static constexpr TileCost rows_cost(Tile256Deep) { return {.25, .1, 2.4, .83, 0.}; }
+static constexpr TileCost rows_cost(Tile320) { return {.28, .1, 2.3, 1.0, 0.}; }
 
 template <class F>
-static void with_rows_tile(int64_t R, int64_t E, int64_t No, F&& f) {
-  const int64_t mean = ceil_div(R, E), full = std::min(R, E);
-  auto fits = [&](int64_t bm, int64_t bn) {
-    return full * ceil_div(mean, bm) * ceil_div(No, bn) >= kGroupedCus;
+static void with_rows_tile(int64_t R, int64_t E, int64_t No, int64_t Kc, bool out_bf16, F&& f) {
+  const double full = (double)std::min(R, E), mean = (double)R / full;
+  const double w_mb = full * No * Kc * 2e-6;
+  const double mb = w_mb + R * (Kc * 2e-6 + No * (out_bf16 ? 2e-6 : 4e-6));
+  const double stages = (double)ceil_div(Kc, 64);
+  auto us = [&](auto s) {
+    using S = decltype(s);
+    const TileCost c = rows_cost(s);
+    double blocks = std::ceil(mean / S::BM);   // of an expert
+    if (E > 1)
+      blocks = mean + 2.5 * std::sqrt(mean) <= S::BM ? 1.0 : std::max(1.0, mean / S::BM + 0.5);
+    const double rounds = std::ceil(full * blocks * ceil_div(No, S::BN) / kSlots<S> - 1e-9);
+    return std::max(4.3 + rounds * (c.ends + stages * c.stage),
+                    mb * c.mb + w_mb * (blocks - 1.0) * c.l2_mb);
   };
-  // mean + 2.5 sqrt(mean) <= bm
-  auto one_block = [&](int64_t bm) {
-    return mean <= bm && 4 * (bm - mean) * (bm - mean) >= 25 * mean;
+  with_least(us, f, TileStream{}, Tile64{}, TilePair{}, Tile128{}, Tile192{}, Tile256Deep{}, Tile320{});
+}
+
+// Weight gradient. Measured (us) with 256 x 256, 128 x 128 and 64 x 128 tiles: 32 experts of 1024 rows,
+// two with 40% of them, 5120 x 5120 fp32, 1783, 2127, 2783; 22 of 42 rows, 2536 x 4432 bf16, 132, 151,
+// 169; 24 of 33 rows, 1656 x 344 fp32, 21, 15, 15. A launch is no shorter than the tiles of its longest
+// expert, which is taken to have four times the mean's rows: 24 experts, one with 7500 of 18850 rows,
+// 1016 x 392, 166, 98, 86. Taken by this rule, the calls it was fitted to take 3% more than each
+// one's best tile.
+using Tile256 = TileShape<256, 256, 2, 4, 2, 2>;
+using TileHalfPair = TileShape<64, 128, 1, 4, 2, 2>;
+static constexpr TileCost dw_cost(Tile256) { return {.205, .10, 3.9, 2.2, 1.4}; }
+static constexpr TileCost dw_cost(TilePair) { return {.20, .06, 2.2, 1.1, .8}; }
+static constexpr TileCost dw_cost(TileHalfPair) { return {.20, .05, 1.8, 1.0, .7}; }
+
+template <class F>
+static void with_dw_tile(int64_t R, int64_t E, int64_t N, int64_t K, bool out_bf16, F&& f) {
+  const double mean = (double)R / E;
+  const double stages = E == 1 ? (double)std::max<int64_t>(1, ceil_div(R, 64))
+                               : std::max(1.0, mean > 32.0 ? mean / 64 + 0.5 : 1.0);
+  const double longest = E == 1 ? stages : 4.0 * stages;
+  const double mb = (double)E * N * K * (out_bf16 ? 2e-6 : 4e-6) + R * (N + K) * 2e-6;
+  auto us = [&](auto s) {
+    using S = decltype(s);
+    const TileCost c = dw_cost(s);
+    const double tiles = (double)ceil_div(N, S::BM) * ceil_div(K, S::BN);
+    const double rounds = std::ceil(E * tiles / kSlots<S> - 1e-9);
+    return std::max({5.3 + rounds * (c.ends + stages * c.stage), 5.3 + c.ends + longest * c.alone,
+                     mb * c.mb + tiles * R * (S::BM + S::BN) * 2e-6 * c.l2_mb});
   };
-  if (mean <= 24 && fits(32, 128))
-    f(TileStream{});
-  else if (one_block(128) && fits(128, 256))
-    f(Tile128{});
-  else if (one_block(192) && fits(192, 256))
-    f(Tile192{});
-  else if (one_block(256) && fits(256, 256))
-    f(Tile256Deep{});
-  else if (mean <= 1536 && fits(320, 256))
-    f(Tile320{});
-  else if (fits(256, 256))
-    f(Tile256{});
-  else
-    f(Tile64{});
+  with_least(us, f, Tile256{}, TilePair{}, TileHalfPair{});
 }
 
 // Blocks that R rows of E experts can make.
@@ -330,19 +384,24 @@ static bool threads_fit(int64_t tiles) {
 }
 
 bool grouped_grid_fits(int64_t R, int64_t E, int64_t N, int64_t K) {
+  // 64 x 128 tiles of 256 threads are the weight gradient's smallest
   bool ok = threads_fit<Tile256>(E * (ceil_div(N, 128) + 7) * (ceil_div(K, 128) + 7));
-  for (int64_t width : {N, K})
-    with_rows_tile(R, E, width, [&](auto s) {
-      using S = decltype(s);
-      ok = ok && threads_fit<S>(max_blocks(R, E, S::BM) * ceil_div(width, S::BN));
-    });
+  for (int64_t width : {N, K}) {
+    // the narrowest tiles' launch fits: so does any
+    if (threads_fit<Tile256>(max_blocks(R, E, 32) * ceil_div(width, 64))) continue;
+    for (bool out_bf16 : {false, true})
+      with_rows_tile(R, E, width, N + K - width, out_bf16, [&](auto s) {
+        using S = decltype(s);
+        ok = ok && threads_fit<S>(max_blocks(R, E, S::BM) * ceil_div(width, S::BN));
+      });
+  }
   return ok;
 }
 
 hipError_t launch_grouped_rows(const void* a, const void* w, const int32_t* offsets, void* out,
                                int R, int E, int No, int Kc, bool w_across, bool out_bf16,
                                hipStream_t st) {
-  with_rows_tile(R, E, No, [&](auto s) {
+  with_rows_tile(R, E, No, Kc, out_bf16, [&](auto s) {
     using S = decltype(s);
     const int64_t blocks = max_blocks(R, E, S::BM);
     const int n_ctiles = (int)ceil_div(No, S::BN);
@@ -363,8 +422,6 @@ hipError_t launch_grouped_rows(const void* a, const void* w, const int32_t* offs
   return hipGetLastError();
 }
 
-using TileDwSmall = TileShape<128, 128, 2, 2, 2, 2>;
-
 template <class S>
 static void launch_dw(const void* dy, const void* x, const int32_t* offsets, void* dw, int R, int E,
                       int N, int K, bool out_bf16, hipStream_t st) {
@@ -383,12 +440,9 @@ static void launch_dw(const void* dy, const void* x, const int32_t* offsets, voi
 
 hipError_t launch_grouped_dw(const void* dy, const void* x, const int32_t* offsets, void* dw, int R,
                              int E, int N, int K, bool out_bf16, hipStream_t st) {
-  // 256 x 256 tiles where they fill the GPU (1.89 ms against 2.21 at the size above, bf16 gradients
-  // 1.64 against 1.88; with few rows both wait for the stores: 48 us for 201 MB)
-  if (E * ceil_div(N, 256) * ceil_div(K, 256) >= kGroupedCus)
-    launch_dw<Tile256>(dy, x, offsets, dw, R, E, N, K, out_bf16, st);
-  else
-    launch_dw<TileDwSmall>(dy, x, offsets, dw, R, E, N, K, out_bf16, st);
+  with_dw_tile(R, E, N, K, out_bf16, [&](auto s) {
+    launch_dw<decltype(s)>(dy, x, offsets, dw, R, E, N, K, out_bf16, st);
+  });
   return hipGetLastError();
 }
 

@@ -105,7 +105,9 @@ def test_against_oracle(op, out_dtype, counts, N, K):
 
 # calls large enough for each of the wide tiles: (experts, mean rows, output width, contraction)
 TILES = [(40, 10, 904, 72), (33, 24, 1032, 200), (32, 70, 2056, 72), (32, 150, 2056, 136),
-         (32, 208, 2184, 72), (16, 300, 2056, 264), (16, 700, 1288, 72), (3, 1700, 3336, 72)]
+         (32, 208, 2184, 72), (16, 300, 2056, 264), (16, 700, 1288, 72), (3, 1700, 3336, 72),
+         (24, 70, 1288, 264), (24, 150, 2056, 72), (24, 200, 1288, 200), (24, 200, 1288, 72),
+         (40, 700, 264, 72)]
 
 
 @pytest.mark.parametrize("op", ["mm", "dx"])
@@ -121,7 +123,8 @@ def test_exact_sums_wide_tiles(op, out_dtype, E, mean, width, depth):
 
 @pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("counts,N,K", [([0, 1, 63, 64, 65, 128, 300] * 4, 1032, 776),
-                                        ([1000], 4104, 4112), ([40] * 65, 520, 264)])
+                                        ([1000], 4104, 4112), ([40] * 65, 520, 264),
+                                        ([70], 4040, 4088), ([65, 0, 100] * 5, 1272, 1016)])
 def test_exact_sums_weight_gradient_tiles(out_dtype, counts, N, K):
     check("dw", counts, N, K, out_dtype, True, first=2, behind=1)
 
