@@ -477,14 +477,11 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
                           mat, row0, col0, smem, wave, lane);
 }
 
-// Small matrices (shorter side <= 64, longer <= 512): all steps in one launch, a workgroup a matrix.
+// Small matrices: all steps in one launch, a workgroup a matrix of up to 16 MT rows and 128 NJ columns.
 // X stays in registers in 32 bits (wave w holds column tiles w, w + 8, ...), its fp16 half for the
-// products in LDS, where the two 64 x 64 matrices lie too; each wave computes two of their 16
-// sub-tiles. The formats and scales are those above, with X itself in lo's place. Bound by latency: one
-// 64 x 512 matrix, five steps, 30 us (80 in a launch a product), 2000 of them 292 us.
-constexpr int kSmallM = 64, kSmallN = 512, kSmallWaves = 8;
-constexpr int kSmallPitch = 2 * kSmallN + 16, kSquarePitch = 2 * kSmallM + 16;   // bytes
-constexpr int kSmallTiles = kSmallN / 16 / kSmallWaves;   // column tiles a wave
+// products in LDS, where A and B lie too; each wave computes an eighth of their sub-tiles. The
+// formats and scales are those above, with X itself in lo's place. Bound by latency.
+constexpr int kSmallWaves = 8;
 
 struct NsSmallArgs {
   const void* g;
@@ -493,13 +490,18 @@ struct NsSmallArgs {
   float a, b, c, ident, eps, scale;
 };
 
+template <int MT, int NJ>
 __global__ __launch_bounds__(64 * kSmallWaves) void ns_small_kernel(NsSmallArgs p) {
+  constexpr int kM = 16 * MT;
+  constexpr int kPitch = 2 * 128 * NJ + 16, kSquarePitch = 2 * kM + 16;   // bytes
+  constexpr int kSquare = kM * kSquarePitch;
+  constexpr bool kOneSquare = MT > 4;   // LDS holds one of A and B
   __shared__ __attribute__((aligned(16))) unsigned char
-      smem[kSmallM * kSmallPitch + 2 * kSmallM * kSquarePitch + 8 * kSmallWaves];
+      smem[kM * kPitch + (kOneSquare ? 1 : 2) * kSquare + 8 * kSmallWaves];
   unsigned char* const xs = smem;
-  unsigned char* const as = xs + kSmallM * kSmallPitch;
-  unsigned char* const bs = as + kSmallM * kSquarePitch;
-  double* const red = reinterpret_cast<double*>(bs + kSmallM * kSquarePitch);
+  unsigned char* const as = xs + kM * kPitch;
+  unsigned char* const bs = kOneSquare ? as : as + kSquare;
+  double* const red = reinterpret_cast<double*>(bs + kSquare);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r15 = lane & 15, g = lane >> 4;
@@ -509,13 +511,13 @@ __global__ __launch_bounds__(64 * kSmallWaves) void ns_small_kernel(NsSmallArgs 
   auto col_tile = [&](int j) { return j * kSmallWaves + wave; };
 
   // x[i][j]: rows 16 i + lane % 16, columns 16 col_tile(j) + 4 (lane / 16) + 0..3
-  floatx4 x[4][kSmallTiles];
+  floatx4 x[MT][NJ];
   double s = 0.0;
   const bool by4 = !p.tall && (n & 3) == 0;   // then four columns are all in or all out, and aligned
 #pragma unroll
-  for (int j = 0; j < kSmallTiles; ++j)
+  for (int j = 0; j < NJ; ++j) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < MT; ++i) {
       const int r = 16 * i + r15, c = 16 * col_tile(j) + 4 * g;
       x[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
       if (r >= m || c >= n) continue;
@@ -536,10 +538,11 @@ __global__ __launch_bounds__(64 * kSmallWaves) void ns_small_kernel(NsSmallArgs 
                             p.g_bf16);
       }
     }
+  }
 #pragma unroll
-  for (int j = 0; j < kSmallTiles; ++j)
+  for (int j = 0; j < NJ; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) s += (double)x[i][j][q] * x[i][j][q];
 #pragma unroll
@@ -552,82 +555,92 @@ __global__ __launch_bounds__(64 * kSmallWaves) void ns_small_kernel(NsSmallArgs 
   const double den = sqrt(s) + (double)p.eps;
   const double mul = den > 0.0 ? (double)p.scale / den : 0.0;   // a zero matrix stays zero
 #pragma unroll
-  for (int j = 0; j < kSmallTiles; ++j)
+  for (int j = 0; j < NJ; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) x[i][j][q] = (float)(x[i][j][q] * mul);
+      for (int q = 0; q < 4; ++q) {
+        float v = x[i][j][q];
+        asm volatile("" : "+v"(v));   // or the 64-bit values of the sum above stay in registers
+        x[i][j][q] = (float)(v * mul);
+      }
 
-  const int r = 16 * (wave >> 1) + r15;   // the wave's sub-tiles of A and B: two of a row
+  // the wave's sub-tiles of A and B: T of a row
+  constexpr int T = MT * MT / kSmallWaves, kRowWaves = MT / T;
+  const int r = 16 * (wave / kRowWaves) + r15, ct = wave % kRowWaves * T;
   auto frag = [&](const unsigned char* at) { return *reinterpret_cast<const intx4*>(at); };
   for (int step = 0; step < p.steps; ++step) {
 #pragma unroll
-    for (int j = 0; j < kSmallTiles; ++j)
+    for (int j = 0; j < NJ; ++j)
       if (col_tile(j) < tiles)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<u32x2*>(xs + (16 * i + r15) * kSmallPitch + 32 * col_tile(j) + 8 * g) =
+        for (int i = 0; i < MT; ++i)
+          *reinterpret_cast<u32x2*>(xs + (16 * i + r15) * kPitch + 32 * col_tile(j) + 8 * g) =
               u32x2{pack_f16(x[i][j].x, x[i][j].y), pack_f16(x[i][j].z, x[i][j].w)};
     __syncthreads();
     // A
-    floatx4 d[2] = {};
+    floatx4 d[T] = {};
 #pragma unroll 2
     for (int k = 0; k < tiles / 2; ++k) {
-      const intx4 fa = frag(xs + r * kSmallPitch + 64 * k + 16 * g);
+      const intx4 fa = frag(xs + r * kPitch + 64 * k + 16 * g);
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < T; ++t)
         d[t] = tile_mma<true>(
-            frag(xs + (16 * (2 * (wave & 1) + t) + r15) * kSmallPitch + 64 * k + 16 * g), fa, d[t]);
+            frag(xs + (16 * (ct + t) + r15) * kPitch + 64 * k + 16 * g), fa, d[t]);
     }
     const float c0 = kGramScale / (p.scale * p.scale);
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int c = 16 * (2 * (wave & 1) + t) + 4 * g;
+    for (int t = 0; t < T; ++t) {
+      const int c = 16 * (ct + t) + 4 * g;
       *reinterpret_cast<u32x2*>(as + r * kSquarePitch + 2 * c) =
           u32x2{pack_f16(d[t].x * c0, d[t].y * c0), pack_f16(d[t].z * c0, d[t].w * c0)};
     }
     __syncthreads();
     // B + s I
+    u32x2 h[T];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int c = 16 * (2 * (wave & 1) + t) + 4 * g;
+    for (int t = 0; t < T; ++t) {
+      const int c = 16 * (ct + t) + 4 * g;
       floatx4 e = {};
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < kM / 32; ++k)
         e = tile_mma<true>(
-            frag(as + (16 * (2 * (wave & 1) + t) + r15) * kSquarePitch + 64 * k + 16 * g),
+            frag(as + (16 * (ct + t) + r15) * kSquarePitch + 64 * k + 16 * g),
             frag(as + r * kSquarePitch + 64 * k + 16 * g), e);
       const f16x4 a = *reinterpret_cast<const f16x4*>(as + r * kSquarePitch + 2 * c);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         e[q] =
             p.c / kGramScale * e[q] + p.b * (float)a[q] + (r == c + q ? p.ident * kGramScale : 0.f);
-      *reinterpret_cast<u32x2*>(bs + r * kSquarePitch + 2 * c) =
-          u32x2{pack_f16(e.x, e.y), pack_f16(e.z, e.w)};
+      h[t] = u32x2{pack_f16(e.x, e.y), pack_f16(e.z, e.w)};
     }
+    if constexpr (kOneSquare) __syncthreads();   // A is read
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+      *reinterpret_cast<u32x2*>(bs + r * kSquarePitch + 32 * (ct + t) + 8 * g) = h[t];
     __syncthreads();
     // X
     const bool last = step + 1 == p.steps;
 #pragma unroll
-    for (int j = 0; j < kSmallTiles; ++j) {
+    for (int j = 0; j < NJ; ++j) {
       if (col_tile(j) >= tiles) continue;
-      floatx4 u[4] = {};
+      floatx4 u[MT] = {};
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < kM / 32; ++k) {
         // columns across the contraction: transposing reads of rows 32 k + 8 g + 0..3 and 4..7
-        const unsigned char* at = xs + (32 * k + 8 * g + (r15 >> 2)) * kSmallPitch +
+        const unsigned char* at = xs + (32 * k + 8 * g + (r15 >> 2)) * kPitch +
                                   32 * col_tile(j) + 8 * (r15 & 3);
         const u32x2 lo = __builtin_bit_cast(
             u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at));
         const u32x2 hi = __builtin_bit_cast(
-            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 4 * kSmallPitch)));
+            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 4 * kPitch)));
         const intx4 fx{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < MT; ++i)
           u[i] = tile_mma<true>(fx, frag(bs + (16 * i + r15) * kSquarePitch + 64 * k + 16 * g), u[i]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float v = x[i][j][q], h = (float)(_Float16)v;
@@ -638,9 +651,9 @@ __global__ __launch_bounds__(64 * kSmallWaves) void ns_small_kernel(NsSmallArgs 
   }
   const float back = 1.f / p.scale;
 #pragma unroll
-  for (int j = 0; j < kSmallTiles; ++j)
+  for (int j = 0; j < NJ; ++j) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < MT; ++i) {
       const int ro = 16 * i + r15, co = 16 * col_tile(j) + 4 * g;
       if (ro >= m || co >= n) continue;
       const floatx4 v = x[i][j] * back;
@@ -655,9 +668,20 @@ __global__ __launch_bounds__(64 * kSmallWaves) void ns_small_kernel(NsSmallArgs 
                 (uint16_t)pack_bf16(v[q], 0.f);
       }
     }
+  }
 }
 
-static bool ns_is_small(int m, int n) { return m <= kSmallM && n <= kSmallN; }
+static bool ns_is_small(int m, int n) { return m <= 64 ? n <= 1024 : m <= 128 && n <= 384; }
+template <class F>
+static void with_ns_small(int m, int n, F&& f) {
+  using std::integral_constant;
+  if (m <= 64)
+    n <= 512 ? f(integral_constant<int, 4>{}, integral_constant<int, 4>{})
+             : f(integral_constant<int, 4>{}, integral_constant<int, 8>{});
+  else
+    n <= 256 ? f(integral_constant<int, 8>{}, integral_constant<int, 2>{})
+             : f(integral_constant<int, 8>{}, integral_constant<int, 3>{});
+}
 
 // ---- host side -----------------------------------------------------------------------------------
 using NsTile256 = TileShape<256, 256, 2, 4, 2, 2>;
@@ -743,8 +767,11 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
   const float sx = x_scale(L.n);
   const float ident = std::round(-(b + c) * 4.f) / 4.f;   // exact in fp16 at the stored scale
   if (ns_is_small(L.m, L.n)) {
-    hipLaunchKernelGGL(ns_small_kernel, dim3(n_mats), dim3(64 * kSmallWaves), 0, st,
-                       NsSmallArgs{g, out, g_bf16, L.tall, L.m, L.n, steps, a, b, c, ident, eps, sx});
+    with_ns_small(L.m, L.n, [&](auto mt, auto nj) {
+      hipLaunchKernelGGL((ns_small_kernel<decltype(mt)::value, decltype(nj)::value>), dim3(n_mats),
+                         dim3(64 * kSmallWaves), 0, st,
+                         NsSmallArgs{g, out, g_bf16, L.tall, L.m, L.n, steps, a, b, c, ident, eps, sx});
+    });
     return hipGetLastError();
   }
   const int64_t count = (int64_t)rows * cols;

@@ -47,17 +47,20 @@ def test_against_oracle(shape, dtype):
 
 @pytest.mark.parametrize("shape", [(300, 20, 33), (64, 512), (512, 64), (63, 511), (64, 513),
                                    (260, 70, 70), (260, 100, 66), (192, 130, 300), (192, 300, 130),
-                                   (200, 131, 137), (200, 137, 131)])
+                                   (200, 131, 137), (200, 137, 131),
+                                   (64, 1024), (3, 1023, 61), (64, 1025), (2, 33, 777), (65, 65),
+                                   (3, 66, 256), (257, 128), (120, 384), (384, 128), (128, 385),
+                                   (300, 101, 203), (260, 70, 392), (260, 392, 100)])
 def test_batches_of_every_tile(shape):
-    # one launch a batch up to 64 x 512; tiles of 64, 128 and 256, the last in column halves too
+    # one launch up to 64 x 1024 and 128 x 384; tiles of 64, 128 and 256, the last in column halves too
     print("orthogonalise", shape, flush=True)
     g = _gauss(*shape, seed=sum(shape), dtype=torch.bfloat16)
     _check(g, bm.orthogonalise(g.cuda()))
 
 
+@pytest.mark.parametrize("m,n", [(200, 320), (60, 90), (63, 1000), (120, 250), (127, 381)])
 @pytest.mark.parametrize("kind", ["rank1", "rank8", "power", "outlier"])
-def test_uneven_spectra(kind):
-    m, n = 200, 320
+def test_uneven_spectra(kind, m, n):
     if kind == "rank1":
         g = _gauss(m, 1, seed=1) @ _gauss(1, n, seed=2)
     elif kind == "rank8":
