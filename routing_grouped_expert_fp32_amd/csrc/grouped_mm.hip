@@ -308,9 +308,12 @@ static void with_least(Us&& us, F&& f, S... tiles) {
 //   320 x 256  (2, 2)   374    362    380    408    451    676    995     55    19
 // Few rows: narrow tiles, many workgroups streaming weights. More: one block an expert if it can be, as
 // every further block reads the weights again (rows spread by about the square root of their mean:
-// 2.5 of it are allowed for); the B operand's third stage covers their latency while LDS lasts.
+// 2.5 of it are allowed for); the B operand's third stage covers their latency while LDS lasts. Fewer
+// tiles than CUs and a long contraction: 32 x 64 tiles with twelve stages (3 experts of 2 rows, 2232 x
+// 4464: 24 us, 64 x 64 29, 32 x 128 39).
 // Taken by this rule, the calls it was fitted to take 7% more than each one's best tile.
 using TileStream = TileShape<32, 128, 1, 4, 4, 4>;
+using TileLone = TileShape<32, 64, 1, 4, 12, 12>;
 using Tile64 = TileShape<64, 64, 1, 2, 3, 3>;
 using TilePair = TileShape<128, 128, 2, 2, 2, 2>;
 using Tile128 = TileShape<128, 256, 2, 4, 2, 3>;
@@ -318,6 +321,7 @@ using Tile192 = TileShape<192, 256, 2, 4, 2, 3>;
 using Tile256Deep = TileShape<256, 256, 2, 4, 2, 3>;
 using Tile320 = TileShape<320, 256, 2, 4, 2, 2>;
 static constexpr TileCost rows_cost(TileStream) { return {.172, .1, 1.8, .41, 0.}; }
+static constexpr TileCost rows_cost(TileLone) { return {.21, .1, 1.7, .25, 0.}; }
 static constexpr TileCost rows_cost(Tile64) { return {.228, .1, 2.3, .34, 0.}; }
 static constexpr TileCost rows_cost(TilePair) { return {.240, .1, 1.7, .82, 0.}; }
 static constexpr TileCost rows_cost(Tile128) { return {.215, .1, 3.2, .50, 0.}; }
@@ -341,7 +345,8 @@ static void with_rows_tile(int64_t R, int64_t E, int64_t No, int64_t Kc, bool ou
     return std::max(4.3 + rounds * (c.ends + stages * c.stage),
                     mb * c.mb + w_mb * (blocks - 1.0) * c.l2_mb);
   };
-  with_least(us, f, TileStream{}, Tile64{}, TilePair{}, Tile128{}, Tile192{}, Tile256Deep{}, Tile320{});
+  with_least(us, f, TileStream{}, TileLone{}, Tile64{}, TilePair{}, Tile128{}, Tile192{}, Tile256Deep{},
+             Tile320{});
 }
 
 // Weight gradient. Measured (us) with 256 x 256, 128 x 128 and 64 x 128 tiles: 32 experts of 1024 rows,

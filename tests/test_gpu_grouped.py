@@ -107,7 +107,8 @@ def test_against_oracle(op, out_dtype, counts, N, K):
 TILES = [(40, 10, 904, 72), (33, 24, 1032, 200), (32, 70, 2056, 72), (32, 150, 2056, 136),
          (32, 208, 2184, 72), (16, 300, 2056, 264), (16, 700, 1288, 72), (3, 1700, 3336, 72),
          (24, 70, 1288, 264), (24, 150, 2056, 72), (24, 200, 1288, 200), (24, 200, 1288, 72),
-         (40, 700, 264, 72)]
+         (40, 700, 264, 72), (3, 10, 264, 520), (9, 50, 264, 2056),
+         (16, 33, 776, 520), (40, 100, 264, 520)]
 
 
 @pytest.mark.parametrize("op", ["mm", "dx"])
