@@ -694,26 +694,64 @@ constexpr int kNsCus = 256;
 static dim3 xcd_grid(int64_t tiles) { return dim3((unsigned)(8 * ceil_div(tiles, 8))); }
 static int64_t triangle(int64_t n) { return n * (n + 1) / 2; }
 
-// The largest tile whose workgroups fill the GPU (256 x 256 ones from three quarters on: they multiply
-// a quarter faster); `count` is their number for a tile side. 2560 x 5120, us, 256 / 128 wide tiles:
-// A of 1, 2, 4, 8 matrices 123 / 58, 120 / 81, 134 / 153, 268 / 301; the update of 1, 8: 83 / 94,
-// 628 / 709. No tile is twice as high as the m rows there are.
+// Time in us of a launch of `count` tiles of a side, `stages` of 64 values of the contraction each: full
+// rounds of the workgroups that the GPU holds (3, 2, 1 a CU), then the rest. A tile's ends and its
+// stage were measured on one to eight matrices of 130 to 5120 rows; against the tile it puts first, us a
+// launch: A of 4 matrices 2000 x 2500 256 wide, 128 +19, 64 +40; of 3 1000 x 3000 64 wide, 128 +11, 256
+// +44; of 2560 x 5120 128 wide, 256 +65, of 8 of them 256 wide, 128 +33; the update of 3 632 x 1656
+// 128 wide, 64 +5, 256 +5, of 2 603 x 1532 64 wide, 128 +3, 256 +10.
+static double ns_launch_us(int side, int64_t count, double stages, bool update) {
+  const double ends = side == 64 ? 2.5 : side == 128 ? 3.0 : update ? 5.0 : 9.0;
+  const int64_t slots = kNsCus * (side == 64 ? 3 : side == 128 ? 2 : 1);
+  auto round = [&](int64_t wgs) {
+    const int64_t each = ceil_div(wgs, kNsCus);   // workgroups a CU
+    const double stage = side == 64    ? each == 1 ? .36 : each == 2 ? .46 : .6
+                         : side == 128 ? each == 1 ? .65 : 1.05
+                         : update      ? .9 + .8 * (double)wgs / kNsCus
+                                       : 1.4;
+    return ends + stages * stage;
+  };
+  const int64_t rest = count % slots;
+  double us = (double)(count / slots) * round(slots);
+  if (rest > 0)   // an update's last wide tiles are split where they leave half the CUs idle
+    us += (update && side == 256 && rest <= kNsCus / 2 ? 0.7 : 1.0) * round(rest);
+  return us;
+}
+
+// Calls f with the tile that is fastest; `count` is the tiles' number for a side.
 template <class Count, class F>
-static void with_ns_tile(int m, Count&& count, F&& f) {
-  if (m > 128 && count(256) >= kNsCus * 3 / 4)
+static void with_ns_tile(bool update, int contraction, Count&& count, F&& f) {
+  const double stages = (double)ceil_div(contraction, 64);
+  auto us = [&](int side) { return ns_launch_us(side, count(side), stages, update); };
+  const double t64 = us(64), t128 = us(128), t256 = us(256);
+  if (t256 < t128 && t256 < t64)
     f(NsTile256{});
-  else if (m > 64 && count(128) >= kNsCus)
+  else if (t128 < t64)
     f(NsTile128{});
   else
     f(NsTile64{});
 }
 
-// Parts of the contraction of A's products: one unless 64 x 64 tiles do not fill the GPU; then up to
-// two workgroups a CU, of at least four stages each.
+// Parts of the contraction of A's products: more than one, of at least four stages each and at most two
+// workgroups of 64 x 64 tiles a CU, where that saves more than the launch that adds them takes
+// (3.5 us and 1 a megabyte of sums). 256 x 5120 update: 125 us, in one part 205; 3 of 632 x 1656: one
+// part saves 22 us of 222 over three.
 static int gram_parts(int64_t n_mats, int m, int k) {
-  const int64_t tiles = n_mats * triangle(ceil_div(m, 64));
-  if (tiles >= kNsCus) return 1;
-  return (int)std::max<int64_t>(1, std::min(2 * kNsCus / tiles, ceil_div(k, 256)));
+  const int64_t tiles = n_mats * triangle(ceil_div(m, 64)), stages = ceil_div(k, 64);
+  const int64_t most = std::min(2 * kNsCus / tiles, ceil_div(k, 256));
+  double best = 1e300;
+  for (int side : {64, 128, 256})
+    best = std::min(best, ns_launch_us(side, n_mats * triangle(ceil_div(m, side)), (double)stages, false));
+  int parts = 1;
+  for (int64_t p = 2; p <= most; ++p) {
+    const double us = ns_launch_us(64, tiles * p, (double)ceil_div(stages, p), false) + 3.5 +
+                      (double)(tiles * p) * (64 * 64 * 4 * 1e-6);
+    if (us < best) {
+      best = us;
+      parts = (int)p;
+    }
+  }
+  return parts;
 }
 
 NsLayout ns_layout(int64_t n_mats, int rows, int cols) {
@@ -800,7 +838,7 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
       hipLaunchKernelGGL((ns_gram_sum_kernel<S>), dim3((unsigned)(n_mats * per * 4)), dim3(256), 0,
                          st, sums, gram, L.m, L.mp, per, used, c0);
     } else {
-      with_ns_tile(L.m, gram_tiles, [&](auto tile) {
+      with_ns_tile(false, L.n, gram_tiles, [&](auto tile) {
         using S = decltype(tile);
         hipLaunchKernelGGL((ns_gram_kernel<S, false>), xcd_grid(gram_tiles(S::BM)),
                            dim3(S::kThreads), 0, st, hi[0], gram, L.m, L.mp, L.ld, L.n,
@@ -808,7 +846,7 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
                            0.f);
       });
     }
-    with_ns_tile(L.m, gram_tiles, [&](auto tile) {
+    with_ns_tile(false, L.m, gram_tiles, [&](auto tile) {
       using S = decltype(tile);
       hipLaunchKernelGGL((ns_gram_kernel<S, true>), xcd_grid(gram_tiles(S::BM)),
                          dim3(S::kThreads), 0, st, gram, poly, L.m, L.mp, L.mp, L.m,
@@ -816,7 +854,7 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
                          ident * kGramScale);
     });
     auto update_tiles = [&](int side) { return n_mats * ceil_div(L.m, side) * ceil_div(L.ld, side); };
-    with_ns_tile(L.m, update_tiles, [&](auto tile) {
+    with_ns_tile(true, L.m, update_tiles, [&](auto tile) {
       using S = decltype(tile);
       const int mt = (int)ceil_div(L.m, S::BM), ct = (int)ceil_div(L.ld, S::BN);
       auto update = [&](auto last) {

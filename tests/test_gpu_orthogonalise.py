@@ -50,7 +50,7 @@ def test_against_oracle(shape, dtype):
                                    (200, 131, 137), (200, 137, 131),
                                    (64, 1024), (3, 1023, 61), (64, 1025), (2, 33, 777), (65, 65),
                                    (3, 66, 256), (257, 128), (120, 384), (384, 128), (128, 385),
-                                   (300, 101, 203), (260, 70, 392), (260, 392, 100)])
+                                   (300, 101, 203), (260, 70, 392), (260, 392, 100), (26, 650, 700)])
 def test_batches_of_every_tile(shape):
     # one launch up to 64 x 1024 and 128 x 384; tiles of 64, 128 and 256, the last in column halves too
     print("orthogonalise", shape, flush=True)
