@@ -314,9 +314,10 @@ BEAM_API size_t beam_residual_boundary_backward_workspace_bytes(int64_t T, int32
  *   coeffs     {a, b, c} (HOST pointer, read before the call returns), each |.| <= 16
  *   steps      >= 1
  *   workspace  device scratch of at least beam_moe_orthogonalise_workspace_bytes(n_mats, rows, cols)
- * The iterates are held as pairs of fp16 (about 22 bits) and the products taken on fp16 with FP32
- * sums: before its last rounding to bf16 the result is within about 0.2% (2-norm) of the exact
- * iteration's for coefficients that keep the singular values near 1. Iterates that grow past fp16
+ * The iterates are held as pairs of fp16 (about 22 bits), each matrix's at a power of two of its own, and
+ * the products taken on fp16 with FP32 sums: before its last rounding to bf16 the result is within
+ * about 0.2% (2-norm) of the exact iteration's for coefficients that keep the singular values near 1,
+ * whatever the norm of G (down to 2^-100 eps). Iterates that grow past fp16
  * (entries beyond 65504 / (2 sqrt(longer side))) come out infinite or NaN.
  * Limits: rows and cols <= 65536, n_mats <= 65535, steps <= 64, and a launch of fewer than 2^32 threads.
  * Equal calls give equal bits. */

@@ -15,7 +15,6 @@ using namespace beam::host;
 constexpr int32_t kMaxGroupedExperts = 4096;
 constexpr int32_t kMaxGroupedWidth = 1 << 20;
 constexpr int32_t kMaxNsSide = 1 << 16;
-constexpr int32_t kMaxNsSteps = 64;
 
 beam_status_t check_grouped_shape(int64_t R, int32_t E, int32_t N, int32_t K, int32_t out_dtype) {
   if (R < 0 || E <= 0 || N <= 0 || K <= 0) return BEAM_ERR_SHAPE;
@@ -171,7 +170,7 @@ beam_status_t beam_moe_orthogonalise(const void* g, int32_t g_dtype, void* out, 
   if (steps < 1 || !(std::isfinite(eps) && eps >= 0.f)) return BEAM_ERR_SHAPE;
   for (int i = 0; i < 3; ++i)   // the stored B + s I must stay inside fp16
     if (!(std::fabs(coeffs[i]) <= 16.f)) return BEAM_ERR_SHAPE;
-  if (steps > kMaxNsSteps) return BEAM_ERR_UNSUPPORTED;
+  if (steps > beam::kNsMaxSteps) return BEAM_ERR_UNSUPPORTED;
   if (n_mats == 0) return BEAM_OK;
   if (!g || !out || !workspace) return BEAM_ERR_NULL;
   if (!aligned16(g) || !aligned16(out) || !aligned16(workspace)) return BEAM_ERR_ALIGN;

@@ -174,10 +174,12 @@ struct BoundaryBwdArgs {
 int boundary_bwd_parts(int64_t T, int H);
 hipError_t launch_boundary_bwd(const BoundaryBwdArgs& a, int64_t T, int H, hipStream_t st);
 
-// Workspace of the orthogonalised update (byte offsets): partial sums of squares, X as hi (two, in
-// turn) + lo, A and B, partial sums of A; m <= n its sides, mp and ld their padded row lengths.
+// Workspace of the orthogonalised update (byte offsets): partial sums of squares, every step's unit of X
+// (kNsMaxSteps a matrix), X as hi (two, in turn) + lo, A and B, partial sums of A; m <= n its sides, mp
+// and ld their padded row lengths.
+constexpr int kNsMaxSteps = 64;
 struct NsLayout {
-  size_t parts = 0, hi[2] = {0, 0}, lo = 0, gram = 0, poly = 0, sums = 0,
+  size_t parts = 0, units = 0, hi[2] = {0, 0}, lo = 0, gram = 0, poly = 0, sums = 0,
          total = 0;
   int m = 0, n = 0, mp = 0, ld = 0;
   bool tall = false;

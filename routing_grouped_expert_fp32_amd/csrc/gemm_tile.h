@@ -50,6 +50,9 @@ struct TileShape {
 // Wave-uniform values that the compiler would otherwise keep in vector registers, where a buffer
 // descriptor made from them costs a loop around every load.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ float uniform(float v) {
+  return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v)));
+}
 template <class T>
 __device__ __forceinline__ T* uniform(T* p) {
   const uint64_t u = (uint64_t)p;

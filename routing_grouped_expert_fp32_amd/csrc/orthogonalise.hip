@@ -12,6 +12,13 @@
 // value on converged directions: entries then shrink as X converges, and their rounding with them
 // (the update takes s back off X exactly). Measured against 64 bits before the last rounding to bf16
 // (which is 0.17%): 0.05 - 0.2%.
+//
+// Where |G|_F is far under eps, X starts far under 1 and would sink below fp16's smallest values (at
+// |G|_F = 1e-5 eps the result was 2% off, from 1e-7 eps on zero). Each matrix therefore holds X times
+// a power of two of its own, 2^j, chosen anew at every step from a bound u on X's singular values:
+// j = 0 from u = 1/2 on, else 2^j u in [1/2, 1). u starts as |G|_F / (|G|_F + eps); a step takes a
+// singular value v to p(v) = a v + b v^3 + c v^5, and u to the largest |p| up to u. A then holds 4^j
+// times its values, B and the update undo that exactly.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -29,6 +36,44 @@ static float x_scale(int n_long) {
   float s = 1.f;
   while (s * s < (float)n_long) s *= 2.f;
   return s;
+}
+
+// 2^-j for a bound u >= 0 on X's norm; NaN gives 1.
+constexpr int kMaxShift = 100;
+__device__ __forceinline__ float ns_unit(float u) {
+  const int e = (int)(__float_as_uint(u) >> 23 & 255) - 126;   // u < 2^e; subnormals -126
+  return __uint_as_float((uint32_t)(127 + min(max(e, -kMaxShift), 0)) << 23);
+}
+__device__ __forceinline__ float pow2_inverse(float unit) {   // of a power of two
+  return __uint_as_float((254u << 23) - __float_as_uint(unit));
+}
+// p and its extrema: |p| is peak[i] at at[i] > 0 (at: infinite where there is none).
+struct NsCurve {
+  float a, b, c, at[2], peak[2];
+};
+static NsCurve ns_curve(float a, float b, float c) {
+  NsCurve p{a, b, c, {INFINITY, INFINITY}, {0.f, 0.f}};
+  // a + 3 b t + 5 c t^2 = 0, t = v^2, by the larger root's form without cancellation
+  const double d = 9.0 * b * b - 20.0 * (double)a * c;
+  const double q = -0.5 * (3.0 * b + std::copysign(std::sqrt(std::max(d, 0.0)), (double)b));
+  const double roots[2] = {c != 0.f ? q / (5.0 * c) : 0.0, q != 0.0 ? a / q : 0.0};
+  if (d >= 0.0)
+    for (int i = 0; i < 2; ++i)
+      if (roots[i] > 0.0 && std::isfinite(roots[i])) {
+        const double t = roots[i], v = std::sqrt(t);
+        p.at[i] = (float)v;
+        p.peak[i] = (float)std::fabs(v * (a + t * (b + t * c)));
+      }
+  return p;
+}
+// The bound after a step. Past 2 it stays there (p reaches past 2 up to 2), and j with it at zero.
+__device__ __forceinline__ float ns_next_bound(float u, const NsCurve& p) {
+  const float t = u * u;
+  float v = fabsf(u * (p.a + t * (p.b + t * p.c)));
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (p.at[i] < u) v = fmaxf(v, p.peak[i]);
+  return fminf(v, 2.f);
 }
 
 __device__ __forceinline__ float load_as_f32(const void* p, int64_t i, bool bf16) {
@@ -85,12 +130,13 @@ __global__ __launch_bounds__(256) void ns_norm_kernel(const void* __restrict__ g
     parts[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = ((red[0] + red[1]) + red[2]) + red[3];
 }
 
-// hi + lo = G * scale / (norm + eps), laid out [m][ld] along the shorter side, zeros in the padding.
-// 64 x 64 tiles through LDS.
+// hi + lo = G * scale * 2^j / (norm + eps), laid out [m][ld] along the shorter side, zeros in the
+// padding, and units[mat][k] = 2^-j of every step k. 64 x 64 tiles through LDS.
 __global__ __launch_bounds__(256) void ns_init_kernel(const void* __restrict__ g, int g_bf16,
                                                       int rows, int cols, int tall, int m, int ld,
                                                       const double* __restrict__ parts, int n_parts,
-                                                      float scale, float eps,
+                                                      float scale, float eps, int steps,
+                                                      NsCurve curve, float* __restrict__ units,
                                                       _Float16* __restrict__ hi,
                                                       _Float16* __restrict__ lo) {
   __shared__ float tile[64][65];
@@ -103,7 +149,14 @@ __global__ __launch_bounds__(256) void ns_init_kernel(const void* __restrict__ g
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
   const double den = sqrt(s) + (double)eps;
-  const double mul = den > 0.0 ? (double)scale / den : 0.0;   // a zero matrix stays zero
+  double mul = den > 0.0 ? (double)scale / den : 0.0;   // a zero matrix stays zero
+  float u = (float)(mul * sqrt(s)) * (1.f / scale);
+  mul *= pow2_inverse(ns_unit(u));
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+    for (int k = 0; k < steps; ++k) {
+      units[mat * kNsMaxSteps + k] = ns_unit(u);
+      u = ns_next_bound(u, curve);
+    }
   const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;   // tile origin in X
   // X(r, c) = G(r, c), or G(c, r) when tall; the tile's rows of G are gr0.., its columns gc0..
   const int gr0 = tall ? c0 : r0, gc0 = tall ? r0 : c0;
@@ -189,11 +242,12 @@ __device__ __forceinline__ void triangle_tile(int t, int& i, int& j) {
 // written to both halves of out [m][mp], the mirrored one in 8-byte pieces after a 4 x 4 transpose
 // between neighbouring lanes (both halves through LDS in long rows: 14 us a 256 x 256 tile slower).
 //   POLY = false: out = D * c0                               (x = hi: A)
-//   POLY = true:  out = b x + D * c0 + ident on the diagonal (x = A:  B + s I)
+//   POLY = true:  out = b x + D * c0 + ident on the diagonal (x = A:  B + s I), with A's factor 4^j
+//                 taken out of b and c0 (`unit` points to the step's 2^-j of the first matrix)
 template <class S, bool POLY>
 __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) void ns_gram_kernel(
     const _Float16* __restrict__ x, _Float16* __restrict__ out, int m, int mp, int ld, int k,
-    int per, int total, float c0, float b, float ident) {
+    int per, int total, float c0, float b, float ident, const float* __restrict__ unit) {
   static_assert(S::BM == S::BN, "square tiles");
   __shared__ __attribute__((aligned(16))) unsigned char smem[S::kLdsBytes];
   const int lane = threadIdx.x & 63;
@@ -201,6 +255,11 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   const int v = xcd_tile(blockIdx.x, total);
   if (v < 0) return;
   const int mat = v / per;
+  if constexpr (POLY) {
+    const float i1 = unit[(int64_t)mat * kNsMaxSteps], i2 = i1 * i1;   // 4^-j
+    b *= i2;
+    c0 = c0 * i2 * i2;
+  }
   int ti, tj;
   triangle_tile(v % per, ti, tj);
   const int row0 = uniform(ti) * S::BM, col0 = uniform(tj) * S::BN;
@@ -327,12 +386,13 @@ __global__ __launch_bounds__(256) void ns_gram_sum_kernel(const float* __restric
 }
 
 // X' = c_lo lo + c_hi hi + c_prod (B + s I) hi, as hi' + lo', or, in the last step, rounded to bf16
-// into `out` in G's own layout.
+// into `out` in G's own layout; `rescale` is the next step's 2^j over this one's (in the last step, 2^-j
+// times c_out).
 template <class S, bool LAST>
 __device__ __forceinline__ void ns_update_tile(
     const _Float16* __restrict__ bmat, const _Float16* __restrict__ hi, _Float16* lo,
     _Float16* __restrict__ hi_out, uint16_t* __restrict__ out, int m, int mp, int n, int ld,
-    float c_prod, float c_hi, float c_lo, float c_out, int tall, int mat, int row0, int col0,
+    float c_prod, float c_hi, float c_lo, float rescale, int tall, int mat, int row0, int col0,
     unsigned char* smem, int wave, int lane) {
   const int64_t x0 = (int64_t)mat * m * ld;
   OperandLoader<S::BM, S::kWaves, false, S::KT> la;
@@ -373,8 +433,8 @@ __device__ __forceinline__ void ns_update_tile(
           floatx4 v;
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            v[q] = c_out * (c_prod * acc[i][j][q] + c_hi * (float)h[i][j][q] +
-                            c_lo * (float)l[i][j][q]);
+            v[q] = rescale * (c_prod * acc[i][j][q] + c_hi * (float)h[i][j][q] +
+                              c_lo * (float)l[i][j][q]);
           // row c + lane % 4 of G's layout, columns r .. r + 3
           const u32x2 t = quad_transpose(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w), lane);
           const int c = c0 + 16 * j + (lane & 3);
@@ -428,7 +488,7 @@ __device__ __forceinline__ void ns_update_tile(
         if (r >= m || c >= ld) return;   // ld % 8 == 0: four columns are all in or all out
 #pragma unroll
         for (int q = 0; q < 4; ++q)   // zero in columns n .. ld - 1
-          v[q] = c_prod * v[q] + c_hi * (float)hv[q] + c_lo * (float)lv[q];
+          v[q] = rescale * (c_prod * v[q] + c_hi * (float)hv[q] + c_lo * (float)lv[q]);
         if constexpr (!LAST) {
           const int64_t at = x0 + (int64_t)r * ld + c;
           const f16x4 nh{(_Float16)v.x, (_Float16)v.y, (_Float16)v.z, (_Float16)v.w};
@@ -440,12 +500,12 @@ __device__ __forceinline__ void ns_update_tile(
         } else if ((n & 3) == 0) {   // 8-byte aligned rows, four columns in or out
           if (c < n)
             *reinterpret_cast<u32x2*>(out + ((int64_t)mat * m + r) * n + c) =
-                u32x2{pack_bf16(c_out * v.x, c_out * v.y), pack_bf16(c_out * v.z, c_out * v.w)};
+                u32x2{pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)};
         } else {
           uint16_t* o = out + (int64_t)mat * m * n;
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            if (c + q < n) o[(int64_t)r * n + c + q] = (uint16_t)pack_bf16(c_out * v[q], 0.f);
+            if (c + q < n) o[(int64_t)r * n + c + q] = (uint16_t)pack_bf16(v[q], 0.f);
         }
       });
 }
@@ -455,7 +515,7 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
     const _Float16* __restrict__ bmat, const _Float16* __restrict__ hi, _Float16* lo,
     _Float16* __restrict__ hi_out, uint16_t* __restrict__ out, int m, int mp, int n, int ld,
     int n_mtiles, int n_ctiles, int total, float c_prod, float c_hi, float c_lo, float c_out,
-    int tall) {
+    int tall, const float* __restrict__ unit) {
   __shared__ __attribute__((aligned(16))) unsigned char smem[S::kLdsBytes];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -464,16 +524,18 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   if (v < 0) return;
   const int mat = v / (n_mtiles * n_ctiles), t = v % (n_mtiles * n_ctiles);
   const int row0 = t % n_mtiles * S::BM, col0 = t / n_mtiles * S::BN;
+  const float* const u = unit + (int64_t)mat * kNsMaxSteps;
+  const float rescale = LAST ? c_out * u[0] : u[0] * pow2_inverse(u[1]);   // exact
   if constexpr (kHalves<S>) {
     if (half >= 0) {
       const int c = col0 + half * (S::BN / 2);
       if (c < ld)
         ns_update_tile<HalfTile<S>, LAST>(bmat, hi, lo, hi_out, out, m, mp, n, ld, c_prod, c_hi, c_lo,
-                                          c_out, tall, mat, row0, c, smem, wave, lane);
+                                          rescale, tall, mat, row0, c, smem, wave, lane);
       return;
     }
   }
-  ns_update_tile<S, LAST>(bmat, hi, lo, hi_out, out, m, mp, n, ld, c_prod, c_hi, c_lo, c_out, tall,
+  ns_update_tile<S, LAST>(bmat, hi, lo, hi_out, out, m, mp, n, ld, c_prod, c_hi, c_lo, rescale, tall,
                           mat, row0, col0, smem, wave, lane);
 }
 
@@ -489,7 +551,8 @@ struct NsSmallArgs {
   const void* g;
   uint16_t* out;
   int g_bf16, tall, m, n, steps;
-  float a, b, c, ident, eps, scale;
+  NsCurve curve;
+  float ident, eps, scale;
 };
 
 template <int MT, int NJ>
@@ -555,7 +618,11 @@ __global__ __launch_bounds__(64 * kSmallWaves) void ns_small_kernel(NsSmallArgs 
 #pragma unroll
   for (int w = 0; w < kSmallWaves; ++w) s += red[w];
   const double den = sqrt(s) + (double)p.eps;
-  const double mul = den > 0.0 ? (double)p.scale / den : 0.0;   // a zero matrix stays zero
+  double mul = den > 0.0 ? (double)p.scale / den : 0.0;   // a zero matrix stays zero
+  const float back = 1.f / p.scale;
+  float bound = uniform((float)(mul * sqrt(s)) * back);
+  float unit = uniform(ns_unit(bound));   // 2^-j
+  mul *= pow2_inverse(unit);
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -599,6 +666,8 @@ __global__ __launch_bounds__(64 * kSmallWaves) void ns_small_kernel(NsSmallArgs 
     }
     __syncthreads();
     // B + s I
+    const float i2 = unit * unit, pb = uniform(p.curve.b * i2),
+                pc = uniform(p.curve.c / kGramScale * i2 * i2);
     u32x2 h[T];
 #pragma unroll
     for (int t = 0; t < T; ++t) {
@@ -612,8 +681,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void ns_small_kernel(NsSmallArgs 
       const f16x4 a = *reinterpret_cast<const f16x4*>(as + r * kSquarePitch + 2 * c);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        e[q] =
-            p.c / kGramScale * e[q] + p.b * (float)a[q] + (r == c + q ? p.ident * kGramScale : 0.f);
+        e[q] = pc * e[q] + pb * (float)a[q] + (r == c + q ? p.ident * kGramScale : 0.f);
       h[t] = u32x2{pack_f16(e.x, e.y), pack_f16(e.z, e.w)};
     }
     if constexpr (kOneSquare) __syncthreads();   // A is read
@@ -623,6 +691,10 @@ __global__ __launch_bounds__(64 * kSmallWaves) void ns_small_kernel(NsSmallArgs 
     __syncthreads();
     // X
     const bool last = step + 1 == p.steps;
+    bound = ns_next_bound(bound, p.curve);
+    const float next = last ? 1.f : uniform(ns_unit(bound)), rescale = unit * pow2_inverse(next);   // exact
+    const float c_prod = rescale / kGramScale, ca = rescale * p.curve.a, cs = rescale * p.ident;
+    unit = next;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       if (col_tile(j) >= tiles) continue;
@@ -647,11 +719,10 @@ __global__ __launch_bounds__(64 * kSmallWaves) void ns_small_kernel(NsSmallArgs 
         for (int q = 0; q < 4; ++q) {
           const float v = x[i][j][q], h = (float)(_Float16)v;
           // a X - s hi + (B + s I) hi, or, in the last step, (a - s) X + (B + s I) hi
-          x[i][j][q] = u[i][q] * (1.f / kGramScale) + p.a * v - p.ident * (last ? v : h);
+          x[i][j][q] = u[i][q] * c_prod + ca * v - cs * (last ? v : h);
         }
     }
   }
-  const float back = 1.f / p.scale;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
 #pragma unroll
@@ -773,6 +844,7 @@ NsLayout ns_layout(int64_t n_mats, int rows, int cols) {
   };
   const size_t x = 2 * (size_t)n_mats * L.m * L.ld, a = 2 * (size_t)n_mats * L.m * L.mp;
   L.parts = take(sizeof(double) * kNormParts * (size_t)n_mats);
+  L.units = take(sizeof(float) * kNsMaxSteps * (size_t)n_mats);
   L.hi[0] = take(x);
   L.hi[1] = take(x);
   L.lo = take(x);
@@ -798,19 +870,21 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
                                 hipStream_t st) {
   const NsLayout L = ns_layout(n_mats, rows, cols);
   double* norm_parts = reinterpret_cast<double*>(ws + L.parts);
+  float* units = reinterpret_cast<float*>(ws + L.units);
   _Float16* hi[2] = {reinterpret_cast<_Float16*>(ws + L.hi[0]),
                      reinterpret_cast<_Float16*>(ws + L.hi[1])};
   _Float16* lo = reinterpret_cast<_Float16*>(ws + L.lo);
   _Float16* gram = reinterpret_cast<_Float16*>(ws + L.gram);
   _Float16* poly = reinterpret_cast<_Float16*>(ws + L.poly);
   const float a = coeffs[0], b = coeffs[1], c = coeffs[2];
+  const NsCurve curve = ns_curve(a, b, c);
   const float sx = x_scale(L.n);
   const float ident = std::round(-(b + c) * 4.f) / 4.f;   // exact in fp16 at the stored scale
   if (ns_is_small(L.m, L.n)) {
     with_ns_small(L.m, L.n, [&](auto mt, auto nj) {
       hipLaunchKernelGGL((ns_small_kernel<decltype(mt)::value, decltype(nj)::value>), dim3(n_mats),
                          dim3(64 * kSmallWaves), 0, st,
-                         NsSmallArgs{g, out, g_bf16, L.tall, L.m, L.n, steps, a, b, c, ident, eps, sx});
+                         NsSmallArgs{g, out, g_bf16, L.tall, L.m, L.n, steps, curve, ident, eps, sx});
     });
     return hipGetLastError();
   }
@@ -821,8 +895,7 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
   hipLaunchKernelGGL(ns_init_kernel,
                      dim3((unsigned)ceil_div(L.ld, 64), (unsigned)ceil_div(L.m, 64), n_mats),
                      dim3(256), 0, st, g, g_bf16, rows, cols, L.tall, L.m, L.ld, norm_parts,
-                     n_parts, sx, eps,
-                     hi[0], lo);
+                     n_parts, sx, eps, steps, curve, units, hi[0], lo);
   const int parts = gram_parts(n_mats, L.m, L.n);
   auto gram_tiles = [&](int side) { return n_mats * triangle(ceil_div(L.m, side)); };
   for (int s = 0; s < steps; ++s) {
@@ -843,7 +916,7 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
         hipLaunchKernelGGL((ns_gram_kernel<S, false>), xcd_grid(gram_tiles(S::BM)),
                            dim3(S::kThreads), 0, st, hi[0], gram, L.m, L.mp, L.ld, L.n,
                            (int)triangle(ceil_div(L.m, S::BM)), (int)gram_tiles(S::BM), c0, 0.f,
-                           0.f);
+                           0.f, nullptr);
       });
     }
     with_ns_tile(false, L.m, gram_tiles, [&](auto tile) {
@@ -851,7 +924,7 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
       hipLaunchKernelGGL((ns_gram_kernel<S, true>), xcd_grid(gram_tiles(S::BM)),
                          dim3(S::kThreads), 0, st, gram, poly, L.m, L.mp, L.mp, L.m,
                          (int)triangle(ceil_div(L.m, S::BM)), (int)gram_tiles(S::BM), c / kGramScale, b,
-                         ident * kGramScale);
+                         ident * kGramScale, units + s);
     });
     auto update_tiles = [&](int side) { return n_mats * ceil_div(L.m, side) * ceil_div(L.ld, side); };
     with_ns_tile(true, L.m, update_tiles, [&](auto tile) {
@@ -865,7 +938,7 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
         hipLaunchKernelGGL((ns_update_kernel<S, kLast>), xcd_grid_halves<S>(update_tiles(S::BM)),
                            dim3(S::kThreads), 0, st, poly, hi[0], lo, hi[1], out, L.m, L.mp, L.n,
                            L.ld, mt, ct, (int)update_tiles(S::BM), 1.f / kGramScale, a - ident, kLast ? a - ident : a,
-                           1.f / sx, L.tall);
+                           1.f / sx, L.tall, units + s);
       };
       if (s + 1 == steps)
         update(std::true_type{});
