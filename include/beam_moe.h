@@ -317,8 +317,9 @@ BEAM_API size_t beam_residual_boundary_backward_workspace_bytes(int64_t T, int32
  * The iterates are held as pairs of fp16 (about 22 bits), each matrix's at a power of two of its own, and
  * the products taken on fp16 with FP32 sums: before its last rounding to bf16 the result is within
  * about 0.2% (2-norm) of the exact iteration's for coefficients that keep the singular values near 1,
- * whatever the norm of G (down to 2^-100 eps). Iterates that grow past fp16
- * (entries beyond 65504 / (2 sqrt(longer side))) come out infinite or NaN.
+ * whatever the norm of G (down to 2^-100 eps). A and b A + c A^2 - (b + c) I are held in fp16 at 256
+ * times their values: if, before a step, a row of X has a norm of 16 or an entry of the latter is 255 in
+ * size, the result is infinite or NaN (the Muon coefficients keep the norms under 1.3).
  * Limits: rows and cols <= 65536, n_mats <= 65535, steps <= 64, and a launch of fewer than 2^32 threads.
  * Equal calls give equal bits. */
 BEAM_API beam_status_t beam_moe_orthogonalise(const void* g, int32_t g_dtype, void* out,

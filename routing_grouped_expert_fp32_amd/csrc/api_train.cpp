@@ -168,7 +168,9 @@ beam_status_t beam_moe_orthogonalise(const void* g, int32_t g_dtype, void* out, 
   if (g_dtype != BEAM_F32 && g_dtype != BEAM_BF16) return BEAM_ERR_DTYPE;
   if (!coeffs) return BEAM_ERR_NULL;
   if (steps < 1 || !(std::isfinite(eps) && eps >= 0.f)) return BEAM_ERR_SHAPE;
-  for (int i = 0; i < 3; ++i)   // the stored B + s I must stay inside fp16
+  // at a norm of 1 the stored B + s I is inside fp16 (|b| + |c| + |s| <= 65 of 255); iterates that the
+  // coefficients let grow may still leave it
+  for (int i = 0; i < 3; ++i)
     if (!(std::fabs(coeffs[i]) <= 16.f)) return BEAM_ERR_SHAPE;
   if (steps > beam::kNsMaxSteps) return BEAM_ERR_UNSUPPORTED;
   if (n_mats == 0) return BEAM_OK;
