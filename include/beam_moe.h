@@ -315,11 +315,17 @@ BEAM_API size_t beam_residual_boundary_backward_workspace_bytes(int64_t T, int32
  *   steps      >= 1
  *   workspace  device scratch of at least beam_moe_orthogonalise_workspace_bytes(n_mats, rows, cols)
  * The iterates are held as pairs of fp16 (about 22 bits), each matrix's at a power of two of its own, and
- * the products taken on fp16 with FP32 sums: before its last rounding to bf16 the result is within
- * about 0.2% (2-norm) of the exact iteration's for coefficients that keep the singular values near 1,
- * whatever the norm of G (down to 2^-100 eps). A and b A + c A^2 - (b + c) I are held in fp16 at 256
- * times their values: if, before a step, a row of X has a norm of 16 or an entry of the latter is 255 in
- * size, the result is infinite or NaN (the Muon coefficients keep the norms under 1.3).
+ * the products taken on fp16 with FP32 sums: before its last rounding to bf16 the result of up to six
+ * steps is within 0.25% (2-norm) of the exact iteration's for coefficients that keep the singular values
+ * near 1, whatever the norm of G (down to 2^-100 eps). Further steps keep that for coefficients that
+ * contract errors there (|p'| < 1, p(v) = a v + b v^3 + c v^5), as (2, -1.5, 0.5) do. The Muon
+ * coefficients (3.4445, -4.775, 2.0315) do not: a G of full rank is off by 0.3% at eight steps, 0.7% at
+ * 16 and 2% at 20 to 64. Nor do any with |a| > 1 where G has no part: roundings, 2^-22 of its norm, grow
+ * by |a| a step there until they are as large as the result (a G of rank one: 0.5% at eight steps of the
+ * Muon coefficients, 5% at ten, all of it from 12 on, where 32 bits throughout lose it too).
+ * A and b A + c A^2 - (b + c) I are held in fp16 at 256 times their values: if, before a step, a row of X
+ * (a column of a G of more rows than columns) has a norm of 16 or an entry of the latter is 255 in size,
+ * the result is infinite or NaN (the Muon coefficients keep the norms under 1.3).
  * Limits: rows and cols <= 65536, n_mats <= 65535, steps <= 64, and a launch of fewer than 2^32 threads.
  * Equal calls give equal bits. */
 BEAM_API beam_status_t beam_moe_orthogonalise(const void* g, int32_t g_dtype, void* out,
