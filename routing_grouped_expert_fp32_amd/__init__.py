@@ -425,6 +425,8 @@ def _grouped(entry, a, b, offsets, R, E, N, K, shape, out, out_dtype, stream):
     with ctx:
         if out is None:
             out = a.new_empty(shape, dtype=odt)
+        if offsets.data_ptr() & 15:   # a view of a longer table: the C ABI takes aligned addresses
+            offsets = offsets.clone()
         rc = getattr(lib(), entry)(a.data_ptr(), b.data_ptr(), offsets.data_ptr(), out.data_ptr(), R,
                                    E, N, K, out_dtype, st)
     if rc != 0:
@@ -435,7 +437,8 @@ def _grouped(entry, a, b, offsets, R, E, N, K, shape, out, out_dtype, stream):
 def grouped_mm(x, w, offsets, out=None, out_dtype=BEAM_BF16, stream=None):
     """beam_moe_grouped_mm: out [R][N], out[r] = x[r] . w[e]^T for the rows offsets[e] ..
     offsets[e + 1] of expert e. x [R][K] and w [E][N][K] bf16, offsets [E + 1] int32. Rows outside
-    the offsets are left as they were (undefined when out is not given)."""
+    the offsets are left as they were (undefined when out is not given). A range of a layer's experts:
+    w[e0:e1] and offsets[e0:e1 + 1] with all rows (that view is copied first where it is not aligned)."""
     (R, K), (E, N, _) = x.shape, w.shape
     _check_tensor("x", x, (R, K), torch.bfloat16)
     _check_tensor("w", w, (E, N, K), torch.bfloat16)
