@@ -5,7 +5,7 @@
 // (each row a run of k: "row" operands) or across it (each row one k, a run of m or n: "column"
 // operands), so the four products Y = X W^T, dX = dY W, dW = dY^T X and X X^T all read their operands
 // where they lie, without a transposed copy.
-//   * A stage carries 64 values of k (or 32, two column operands). Both kinds reach LDS by 16-byte direct loads, 1 KB a wave
+//   * A stage carries 64 values of k. Both kinds reach LDS by 16-byte direct loads, 1 KB a wave
 //     instruction. Row operands: [rows][64 k], chunk c of row r at c ^ (r & 7), fragments by 16-byte
 //     reads (8 consecutive k of one row). Column operands: [k][rows], the 32-byte unit u of row k
 //     at u ^ f(k), f = (k & 3) | (k >> 3 & 1) << 2 (64 rows: its upper two bits, two stored rows being
@@ -28,18 +28,18 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 // Workgroup tile of BM x BN, WM x WN waves; LDS rings of AST stages of the A operand and BST of B
-// (AST <= BST: B is the one that streams from HBM, A's rows are shared by neighbouring tiles), of KT
+// (AST <= BST: B is the one that streams from HBM, A's rows are shared by neighbouring tiles), of kStageK
 // values of k each.
 // Row sub-tiles (16 rows) are dealt to the wave rows in turn, so that a partly filled tile loads them
 // alike.
-template <int BM_, int BN_, int WM_, int WN_, int AST_, int BST_, int KT_ = 64>
+constexpr int kStageK = 64;
+template <int BM_, int BN_, int WM_, int WN_, int AST_, int BST_>
 struct TileShape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, AST = AST_, BST = BST_, KT = KT_;
-  static_assert(KT == 32 || KT == 64, "a row operand's swizzle is made for 64");
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, AST = AST_, BST = BST_;
   static_assert(2 <= AST && AST <= BST, "ring depths");
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int FM = BM / 16 / WM, FN = BN / 16 / WN;   // 16 x 16 sub-tiles of a wave
-  static constexpr int kABytes = BM * 2 * KT, kBBytes = BN * 2 * KT;
+  static constexpr int kABytes = BM * 2 * kStageK, kBBytes = BN * 2 * kStageK;
   static constexpr int kLdsBytes = AST * kABytes + BST * kBBytes;
   static_assert(kLdsBytes <= 160 * 1024, "LDS budget");
   static_assert(FM * 16 * WM == BM && FN * 16 * WN == BN, "whole sub-tiles");
@@ -75,11 +75,10 @@ __device__ __forceinline__ int column_swizzle(int low, int bit3) {
 }
 
 // Direct loads of one operand's stages (ROWS = BM or BN).
-template <int ROWS, int WAVES, bool COL, int KT>
+template <int ROWS, int WAVES, bool COL>
 struct OperandLoader {
-  static constexpr int L = ROWS * KT / 512 / WAVES;   // 1 KB loads of a wave in a stage
-  static_assert(L * 512 * WAVES == ROWS * KT, "loads split evenly over waves");
-  static_assert(COL || KT == 64, "the swizzle of row operands is made for 128-byte rows");
+  static constexpr int L = ROWS * kStageK / 512 / WAVES;   // 1 KB loads of a wave in a stage
+  static_assert(L * 512 * WAVES == ROWS * kStageK, "loads split evenly over waves");
   static constexpr int kRowChunks = COL ? ROWS / 8 : 8;       // 16-byte chunks of a stored row
   static constexpr int kLoadRows = 64 / kRowChunks;           // stored rows of a load
   static_assert(!COL || (ROWS >= 64 && (ROWS & (ROWS - 1)) == 0), "the swizzle permutes 4 or 8 units");
@@ -114,9 +113,9 @@ struct OperandLoader {
   template <int kAux>
   __device__ __forceinline__ void issue_as(int kt, int64_t k, unsigned char* dst, int wave) const {
     if constexpr (COL) {
-      const int64_t left = k - (int64_t)kt * KT;
-      const int rows = left < KT ? (int)left : KT;
-      const unsigned char* base = uniform(op.base + (int64_t)kt * KT * op.ld);
+      const int64_t left = k - (int64_t)kt * kStageK;
+      const int rows = left < kStageK ? (int)left : kStageK;
+      const unsigned char* base = uniform(op.base + (int64_t)kt * kStageK * op.ld);
       const uint32_t bytes =
           (uint32_t)uniform(rows > 0 ? (int)((rows - 1) * op.ld + op.tail) : 0);
 #pragma unroll
@@ -125,10 +124,10 @@ struct OperandLoader {
     } else {
       const uint32_t bytes = (uint32_t)(op.rows * op.ld);
       // chunks past k: an offset past every buffer (a tile's rows are under 2 GiB)
-      const uint32_t past = (int64_t)kt * KT + kofs < k ? 0u : 0x80000000u;
+      const uint32_t past = (int64_t)kt * kStageK + kofs < k ? 0u : 0x80000000u;
 #pragma unroll
       for (int q = 0; q < L; ++q)
-        buffer_load_lds16<kAux>(op.base, bytes, voff[q] | past, (uint32_t)kt * (2 * KT),
+        buffer_load_lds16<kAux>(op.base, bytes, voff[q] | past, (uint32_t)kt * (2 * kStageK),
                              (lds_void_t*)(dst + (wave * L + q) * 1024));
     }
   }
@@ -197,7 +196,7 @@ __device__ __forceinline__ void tile_barrier() {
 // this one's last MFMAs.
 template <class S, bool ACOL, bool BCOL, bool F16, int NV>
 struct TileStage {
-  static constexpr int STEPS = S::KT / 32, P = STEPS * NV, AHEAD = NV < 4 ? NV : 4;
+  static constexpr int STEPS = kStageK / 32, P = STEPS * NV, AHEAD = NV < 4 ? NV : 4;
   FragReader<S::BM, NV, S::WM, ACOL> ra;
   FragReader<S::BN, S::FN, 1, BCOL> rb;
   intx4 af[P + AHEAD], bf[STEPS + 1][S::FN];   // the next stage's first ones at the end
@@ -261,16 +260,16 @@ __device__ __forceinline__ void tile_zero(floatx4 (&acc)[S::FM][S::FN]) {
 
 // The loop over k of one tile.
 template <class S, bool ACOL, bool BCOL, bool F16, int NV>
-__device__ __forceinline__ void tile_kloop(const OperandLoader<S::BM, S::kWaves, ACOL, S::KT>& la,
-                                           const OperandLoader<S::BN, S::kWaves, BCOL, S::KT>& lb,
+__device__ __forceinline__ void tile_kloop(const OperandLoader<S::BM, S::kWaves, ACOL>& la,
+                                           const OperandLoader<S::BN, S::kWaves, BCOL>& lb,
                                            int64_t k, unsigned char* smem, int wave, int lane,
                                            floatx4 (&acc)[S::FM][S::FN]) {
-  const int nk = (int)((k + S::KT - 1) / S::KT);
+  const int nk = (int)((k + kStageK - 1) / kStageK);
   if (nk == 0) return;
   unsigned char* const aring = smem;
   unsigned char* const bring = smem + S::AST * S::kABytes;
-  constexpr int LA = OperandLoader<S::BM, S::kWaves, ACOL, S::KT>::L;
-  constexpr int LB = OperandLoader<S::BN, S::kWaves, BCOL, S::KT>::L;
+  constexpr int LA = OperandLoader<S::BM, S::kWaves, ACOL>::L;
+  constexpr int LB = OperandLoader<S::BN, S::kWaves, BCOL>::L;
   static_assert(S::BST * (LA + LB) < 64, "vmcnt range");
   // a wave's loads are issued, and counted, in the order A(t), B(t + BST - AST): behind the loads of
   // stage t + 1 came B's of that turn, if B runs ahead, and both operands' of AST - 2 turns
@@ -324,7 +323,7 @@ __device__ __forceinline__ int xcd_tile(int wg, int total) {
 // 447 with halves.
 constexpr int kXcdCus = 32;
 template <class S>
-using HalfTile = TileShape<S::BM, S::BN / 2, S::WM, S::WN, S::AST, S::BST, S::KT>;
+using HalfTile = TileShape<S::BM, S::BN / 2, S::WM, S::WN, S::AST, S::BST>;
 template <class S>
 constexpr bool kHalves = S::BN == 256 && S::kLdsBytes > 80 * 1024;
 template <class S>

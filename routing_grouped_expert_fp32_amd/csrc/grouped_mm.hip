@@ -126,8 +126,8 @@ __device__ __forceinline__ void grouped_rows_tile(const unsigned char* __restric
                                                   unsigned char* smem, int wave, int lane) {
   const int64_t wbytes = (int64_t)No * Kc * 2;
   const int64_t a_ld = (int64_t)Kc * 2;
-  OperandLoader<S::BM, S::kWaves, false, S::KT> la;
-  OperandLoader<S::BN, S::kWaves, WCOL, S::KT> lb;
+  OperandLoader<S::BM, S::kWaves, false> la;
+  OperandLoader<S::BN, S::kWaves, WCOL> lb;
   lb.stream = blk.n_blocks == 1;   // weights that no other block reads need not stay in L2
   la.init({a + (int64_t)blk.row0 * a_ld, a_ld, blk.rows, 0}, wave, lane);
   if constexpr (WCOL)
@@ -259,8 +259,8 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   const int sz = min(kTileGroup, n_mtiles - m0), at = t - m0 * n_ctiles;
   const int row0 = (m0 + at % sz) * S::BM, col0 = at / sz * S::BN;
   const int64_t a_ld = (int64_t)N * 2, b_ld = (int64_t)K * 2;
-  OperandLoader<S::BM, S::kWaves, true, S::KT> la;
-  OperandLoader<S::BN, S::kWaves, true, S::KT> lb;
+  OperandLoader<S::BM, S::kWaves, true> la;
+  OperandLoader<S::BN, S::kWaves, true> lb;
   la.init({dy + begin * a_ld + (int64_t)row0 * 2, a_ld, 0, (N - row0) * 2}, wave, lane);
   lb.init({x + begin * b_ld + (int64_t)col0 * 2, b_ld, 0, (K - col0) * 2}, wave, lane);
   floatx4 acc[S::FM][S::FN];

@@ -265,8 +265,8 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   const int row0 = uniform(ti) * S::BM, col0 = uniform(tj) * S::BN;
   const _Float16* xm = x + (int64_t)mat * m * ld;
   const int64_t ldb = (int64_t)ld * 2;
-  OperandLoader<S::BM, S::kWaves, false, S::KT> la;
-  OperandLoader<S::BN, S::kWaves, false, S::KT> lb;
+  OperandLoader<S::BM, S::kWaves, false> la;
+  OperandLoader<S::BN, S::kWaves, false> lb;
   const auto* xb = reinterpret_cast<const unsigned char*>(xm);
   la.init({xb + row0 * ldb, ldb, min(S::BM, m - row0), 0}, wave, lane);
   lb.init({xb + col0 * ldb, ldb, min(S::BN, m - col0), 0}, wave, lane);
@@ -335,8 +335,8 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   const int row0 = uniform(ti) * S::BM, col0 = uniform(tj) * S::BN;
   const int64_t ldb = (int64_t)ld * 2;
   const auto* xb = reinterpret_cast<const unsigned char*>(x + (int64_t)mat * m * ld + part * kp);
-  OperandLoader<S::BM, S::kWaves, false, S::KT> la;
-  OperandLoader<S::BN, S::kWaves, false, S::KT> lb;
+  OperandLoader<S::BM, S::kWaves, false> la;
+  OperandLoader<S::BN, S::kWaves, false> lb;
   // (a part's last row may reach past the matrix by the offset of the part: its loads past k are
   // kept out by k, not by the buffer's end)
   la.init({xb + row0 * ldb, ldb, min(S::BM, m - row0), 0}, wave, lane);
@@ -395,8 +395,8 @@ __device__ __forceinline__ void ns_update_tile(
     float c_prod, float c_hi, float c_lo, float rescale, int tall, int mat, int row0, int col0,
     unsigned char* smem, int wave, int lane) {
   const int64_t x0 = (int64_t)mat * m * ld;
-  OperandLoader<S::BM, S::kWaves, false, S::KT> la;
-  OperandLoader<S::BN, S::kWaves, true, S::KT> lb;
+  OperandLoader<S::BM, S::kWaves, false> la;
+  OperandLoader<S::BN, S::kWaves, true> lb;
   la.init({reinterpret_cast<const unsigned char*>(bmat + (int64_t)mat * m * mp) +
                (int64_t)row0 * mp * 2,
            (int64_t)mp * 2, min(S::BM, m - row0), 0},
