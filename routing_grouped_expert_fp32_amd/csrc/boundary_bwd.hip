@@ -17,6 +17,7 @@
 #include <type_traits>
 
 #include "device_common.h"
+#include "train_rules.h"
 
 namespace beam {
 
@@ -194,12 +195,6 @@ __global__ __launch_bounds__(64 * kReduceRows) void gamma_reduce_kernel(
   }
 }
 
-// Threads of a workgroup and workgroups of the first launch (two a CU at 256 threads) for rows of H.
-static int bwd_threads(int H) { return H <= 5 * 1024 ? 256 : H <= 5 * 2048 ? 512 : 1024; }
-int boundary_bwd_parts(int64_t T, int H) {
-  return (int)std::min<int64_t>(T, bwd_threads(H) == 256 ? 512 : 256);
-}
-
 hipError_t launch_boundary_bwd(const BoundaryBwdArgs& a, int64_t T, int H, hipStream_t st) {
   const int n_parts = boundary_bwd_parts(T, H);
   auto reduce = [&]() {
@@ -224,7 +219,7 @@ hipError_t launch_boundary_bwd(const BoundaryBwdArgs& a, int64_t T, int H, hipSt
     reduce();
     return hipGetLastError();
   }
-  const int th = bwd_threads(H), need = (int)ceil_div(H, 4 * th);
+  const int th = boundary_bwd_threads(H), need = (int)ceil_div(H, 4 * th);
   auto chunks = [&](auto th_tag) {
     if (need <= 1)
       go(th_tag, std::integral_constant<int, 1>{});

@@ -19,6 +19,7 @@
 #pragma once
 
 #include "device_common.h"
+#include "train_rules.h"
 
 namespace beam {
 
@@ -26,26 +27,6 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-
-// Workgroup tile of BM x BN, WM x WN waves; LDS rings of AST stages of the A operand and BST of B
-// (AST <= BST: B is the one that streams from HBM, A's rows are shared by neighbouring tiles), of kStageK
-// values of k each.
-// Row sub-tiles (16 rows) are dealt to the wave rows in turn, so that a partly filled tile loads them
-// alike.
-constexpr int kStageK = 64;
-template <int BM_, int BN_, int WM_, int WN_, int AST_, int BST_>
-struct TileShape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, AST = AST_, BST = BST_;
-  static_assert(2 <= AST && AST <= BST, "ring depths");
-  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
-  static constexpr int FM = BM / 16 / WM, FN = BN / 16 / WN;   // 16 x 16 sub-tiles of a wave
-  static constexpr int kABytes = BM * 2 * kStageK, kBBytes = BN * 2 * kStageK;
-  static constexpr int kLdsBytes = AST * kABytes + BST * kBBytes;
-  static_assert(kLdsBytes <= 160 * 1024, "LDS budget");
-  static_assert(FM * 16 * WM == BM && FN * 16 * WN == BN, "whole sub-tiles");
-  // sub-tile i of wave row wm
-  __device__ static constexpr int row_tile(int wm, int i) { return wm + WM * i; }
-};
 
 // Wave-uniform values that the compiler would otherwise keep in vector registers, where a buffer
 // descriptor made from them costs a loop around every load.
@@ -308,42 +289,6 @@ __device__ __forceinline__ void tile_kloop(const OperandLoader<S::BM, S::kWaves,
     ia = ja;
     ib = jb;
   }
-}
-
-// Tile v of `total` for workgroup `wg` of a grid of 8 ceil(total / 8), one run of tiles per XCD.
-__device__ __forceinline__ int xcd_tile(int wg, int total) {
-  const int per = (total + 7) >> 3, local = wg >> 3;
-  const int v = (wg & 7) * per + local;
-  return local < per && v < total ? v : -1;
-}
-
-// The same where tiles 256 columns wide have a CU each: a last round of at most half an XCD's CUs would
-// leave the others idle, so its tiles are split into two column halves (`half` 0 or 1, else -1),
-// which take about 0.6 of a tile's time. Two and a half rounds of 320 x 256 tiles: 467 us as three,
-// 447 with halves.
-constexpr int kXcdCus = 32;
-template <class S>
-using HalfTile = TileShape<S::BM, S::BN / 2, S::WM, S::WN, S::AST, S::BST>;
-template <class S>
-constexpr bool kHalves = S::BN == 256 && S::kLdsBytes > 80 * 1024;
-template <class S>
-__device__ __forceinline__ int xcd_tile_halves(int wg, int total, int& half) {
-  const int per = (total + 7) >> 3, first = (wg & 7) * per;
-  const int mine = min(per, total - first);   // tiles of this XCD
-  int local = wg >> 3;
-  half = -1;
-  if constexpr (kHalves<S>) {
-    const int tail = mine % kXcdCus, whole = mine - tail;
-    if (mine > 0 && tail <= kXcdCus / 2 && local >= whole) {
-      half = (local - whole) & 1;
-      local = whole + ((local - whole) >> 1);
-    }
-  }
-  return local < mine ? first + local : -1;
-}
-template <class S>
-static dim3 xcd_grid_halves(int64_t tiles) {
-  return dim3((unsigned)(8 * (ceil_div(tiles, 8) + (kHalves<S> ? kXcdCus / 2 : 0))));
 }
 
 // Hands a tile's accumulators (NV row sub-tiles a wave) on in row order: put(i, j, p) writes the lane's

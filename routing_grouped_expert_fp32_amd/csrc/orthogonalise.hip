@@ -27,7 +27,6 @@
 
 namespace beam {
 
-constexpr int kNormParts = 512;         // most partial sums of squares of a matrix
 constexpr float kGramScale = 256.f;     // A and B hold 2^8 times their values
 
 // X holds 2^k times its values, 2^k about sqrt(longer side): a matrix of orthonormal rows has entries
@@ -744,7 +743,6 @@ __global__ __launch_bounds__(64 * kSmallWaves) void ns_small_kernel(NsSmallArgs 
   }
 }
 
-static bool ns_is_small(int m, int n) { return m <= 64 ? n <= 1024 : m <= 128 && n <= 384; }
 template <class F>
 static void with_ns_small(int m, int n, F&& f) {
   using std::integral_constant;
@@ -757,114 +755,6 @@ static void with_ns_small(int m, int n, F&& f) {
 }
 
 // ---- host side -----------------------------------------------------------------------------------
-using NsTile256 = TileShape<256, 256, 2, 4, 2, 2>;
-using NsTile128 = TileShape<128, 128, 2, 2, 2, 2>;
-using NsTile64 = TileShape<64, 64, 1, 2, 3, 3>;
-constexpr int kNsCus = 256;
-
-static dim3 xcd_grid(int64_t tiles) { return dim3((unsigned)(8 * ceil_div(tiles, 8))); }
-static int64_t triangle(int64_t n) { return n * (n + 1) / 2; }
-
-// Time in us of a launch of `count` tiles of a side, `stages` of 64 values of the contraction each: full
-// rounds of the workgroups that the GPU holds (3, 2, 1 a CU), then the rest. A tile's ends and its
-// stage were measured on one to eight matrices of 130 to 5120 rows; against the tile it puts first, us a
-// launch: A of 4 matrices 2000 x 2500 256 wide, 128 +19, 64 +40; of 3 1000 x 3000 64 wide, 128 +11, 256
-// +44; of 2560 x 5120 128 wide, 256 +65, of 8 of them 256 wide, 128 +33; the update of 3 632 x 1656
-// 128 wide, 64 +5, 256 +5, of 2 603 x 1532 64 wide, 128 +3, 256 +10.
-static double ns_launch_us(int side, int64_t count, double stages, bool update) {
-  const double ends = side == 64 ? 2.5 : side == 128 ? 3.0 : update ? 5.0 : 9.0;
-  const int64_t slots = kNsCus * (side == 64 ? 3 : side == 128 ? 2 : 1);
-  auto round = [&](int64_t wgs) {
-    const int64_t each = ceil_div(wgs, kNsCus);   // workgroups a CU
-    const double stage = side == 64    ? each == 1 ? .36 : each == 2 ? .46 : .6
-                         : side == 128 ? each == 1 ? .65 : 1.05
-                         : update      ? .9 + .8 * (double)wgs / kNsCus
-                                       : 1.4;
-    return ends + stages * stage;
-  };
-  const int64_t rest = count % slots;
-  double us = (double)(count / slots) * round(slots);
-  if (rest > 0)   // an update's last wide tiles are split where they leave half the CUs idle
-    us += (update && side == 256 && rest <= kNsCus / 2 ? 0.7 : 1.0) * round(rest);
-  return us;
-}
-
-// Calls f with the tile that is fastest; `count` is the tiles' number for a side.
-template <class Count, class F>
-static void with_ns_tile(bool update, int contraction, Count&& count, F&& f) {
-  const double stages = (double)ceil_div(contraction, 64);
-  auto us = [&](int side) { return ns_launch_us(side, count(side), stages, update); };
-  const double t64 = us(64), t128 = us(128), t256 = us(256);
-  if (t256 < t128 && t256 < t64)
-    f(NsTile256{});
-  else if (t128 < t64)
-    f(NsTile128{});
-  else
-    f(NsTile64{});
-}
-
-// Parts of the contraction of A's products: more than one, of at least four stages each and at most two
-// workgroups of 64 x 64 tiles a CU, where that saves more than the launch that adds them takes
-// (3.5 us and 1 a megabyte of sums). 256 x 5120 update: 125 us, in one part 205; 3 of 632 x 1656: one
-// part saves 22 us of 222 over three.
-static int gram_parts(int64_t n_mats, int m, int k) {
-  const int64_t tiles = n_mats * triangle(ceil_div(m, 64)), stages = ceil_div(k, 64);
-  const int64_t most = std::min(2 * kNsCus / tiles, ceil_div(k, 256));
-  double best = 1e300;
-  for (int side : {64, 128, 256})
-    best = std::min(best, ns_launch_us(side, n_mats * triangle(ceil_div(m, side)), (double)stages, false));
-  int parts = 1;
-  for (int64_t p = 2; p <= most; ++p) {
-    const double us = ns_launch_us(64, tiles * p, (double)ceil_div(stages, p), false) + 3.5 +
-                      (double)(tiles * p) * (64 * 64 * 4 * 1e-6);
-    if (us < best) {
-      best = us;
-      parts = (int)p;
-    }
-  }
-  return parts;
-}
-
-NsLayout ns_layout(int64_t n_mats, int rows, int cols) {
-  NsLayout L;
-  L.tall = rows > cols;
-  L.m = std::min(rows, cols);
-  L.n = std::max(rows, cols);
-  L.mp = (L.m + 7) / 8 * 8;
-  L.ld = (L.n + 7) / 8 * 8;
-  if (ns_is_small(L.m, L.n)) {   // uses none
-    L.total = 16;
-    return L;
-  }
-  size_t off = 0;
-  auto take = [&](size_t bytes) {
-    const size_t o = off;
-    off += (bytes + 255) & ~size_t(255);
-    return o;
-  };
-  const size_t x = 2 * (size_t)n_mats * L.m * L.ld, a = 2 * (size_t)n_mats * L.m * L.mp;
-  L.parts = take(sizeof(double) * kNormParts * (size_t)n_mats);
-  L.units = take(sizeof(float) * kNsMaxSteps * (size_t)n_mats);
-  L.hi[0] = take(x);
-  L.hi[1] = take(x);
-  L.lo = take(x);
-  L.gram = take(a);
-  L.poly = take(a);
-  const int np = gram_parts(n_mats, L.m, L.n);
-  if (np > 1)
-    L.sums = take(sizeof(float) * 64 * 64 * (size_t)(np * n_mats * triangle(ceil_div(L.m, 64))));
-  L.total = off;
-  return L;
-}
-
-bool ns_grid_fits(int64_t n_mats, int rows, int cols) {
-  // 64 x 64 tiles of 128 threads; wider ones have fewer of both together. A launch counts its threads
-  // in 32 bits.
-  const int64_t mt = ceil_div(std::min(rows, cols), 64), ct = ceil_div(std::max(rows, cols), 64);
-  return n_mats <= 65535 &&
-         (n_mats * mt * std::max(ct, (mt + 1) / 2) + 8 * kXcdCus) * 512 < (int64_t(1) << 32);
-}
-
 hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n_mats, int rows,
                                 int cols, int steps, const float* coeffs, float eps, char* ws,
                                 hipStream_t st) {
@@ -889,41 +779,39 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
     return hipGetLastError();
   }
   const int64_t count = (int64_t)rows * cols;
-  const int n_parts = (int)std::min<int64_t>(kNormParts, ceil_div(count, 8192));
+  const int n_parts = ns_norm_parts(count);
   hipLaunchKernelGGL(ns_norm_kernel, dim3(n_parts, n_mats), dim3(256), 0, st, g, g_bf16, count,
                      norm_parts);
   hipLaunchKernelGGL(ns_init_kernel,
                      dim3((unsigned)ceil_div(L.ld, 64), (unsigned)ceil_div(L.m, 64), n_mats),
                      dim3(256), 0, st, g, g_bf16, rows, cols, L.tall, L.m, L.ld, norm_parts,
                      n_parts, sx, eps, steps, curve, units, hi[0], lo);
-  const int parts = gram_parts(n_mats, L.m, L.n);
-  auto gram_tiles = [&](int side) { return n_mats * triangle(ceil_div(L.m, side)); };
+  const GramParts split = gram_parts(n_mats, L.m, L.n);
+  auto gram_tiles = [&](int side) { return n_mats * ns_triangle(ceil_div(L.m, side)); };
   for (int s = 0; s < steps; ++s) {
     const float c0 = kGramScale / (sx * sx);
-    if (parts > 1) {
+    if (split.parts > 1) {
       using S = NsTile64;
       float* sums = reinterpret_cast<float*>(ws + L.sums);
-      const int per = (int)triangle(ceil_div(L.m, 64));
-      const int kp = (int)ceil_div(ceil_div(L.n, parts), 64) * 64;
-      const int used = (int)ceil_div(L.n, kp);   // rounding to stages can leave fewer parts
-      hipLaunchKernelGGL((ns_gram_part_kernel<S>), dim3((unsigned)(n_mats * per * used)),
-                         dim3(S::kThreads), 0, st, hi[0], sums, L.m, L.ld, L.n, per, used, kp);
+      const int per = (int)ns_triangle(ceil_div(L.m, 64));
+      hipLaunchKernelGGL((ns_gram_part_kernel<S>), dim3((unsigned)(n_mats * per * split.parts)),
+                         dim3(S::kThreads), 0, st, hi[0], sums, L.m, L.ld, L.n, per, split.parts, split.kp);
       hipLaunchKernelGGL((ns_gram_sum_kernel<S>), dim3((unsigned)(n_mats * per * 4)), dim3(256), 0,
-                         st, sums, gram, L.m, L.mp, per, used, c0);
+                         st, sums, gram, L.m, L.mp, per, split.parts, c0);
     } else {
       with_ns_tile(false, L.n, gram_tiles, [&](auto tile) {
         using S = decltype(tile);
-        hipLaunchKernelGGL((ns_gram_kernel<S, false>), xcd_grid(gram_tiles(S::BM)),
+        hipLaunchKernelGGL((ns_gram_kernel<S, false>), dim3((unsigned)xcd_workgroups(gram_tiles(S::BM))),
                            dim3(S::kThreads), 0, st, hi[0], gram, L.m, L.mp, L.ld, L.n,
-                           (int)triangle(ceil_div(L.m, S::BM)), (int)gram_tiles(S::BM), c0, 0.f,
+                           (int)ns_triangle(ceil_div(L.m, S::BM)), (int)gram_tiles(S::BM), c0, 0.f,
                            0.f, nullptr);
       });
     }
     with_ns_tile(false, L.m, gram_tiles, [&](auto tile) {
       using S = decltype(tile);
-      hipLaunchKernelGGL((ns_gram_kernel<S, true>), xcd_grid(gram_tiles(S::BM)),
+      hipLaunchKernelGGL((ns_gram_kernel<S, true>), dim3((unsigned)xcd_workgroups(gram_tiles(S::BM))),
                          dim3(S::kThreads), 0, st, gram, poly, L.m, L.mp, L.mp, L.m,
-                         (int)triangle(ceil_div(L.m, S::BM)), (int)gram_tiles(S::BM), c / kGramScale, b,
+                         (int)ns_triangle(ceil_div(L.m, S::BM)), (int)gram_tiles(S::BM), c / kGramScale, b,
                          ident * kGramScale, units + s);
     });
     auto update_tiles = [&](int side) { return n_mats * ceil_div(L.m, side) * ceil_div(L.ld, side); };
@@ -935,7 +823,7 @@ hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n
         // weak directions, or (B + s I) lo, which vanishes in converged ones; only the last step's
         // error is not amplified in the weak ones
         constexpr bool kLast = decltype(last)::value;
-        hipLaunchKernelGGL((ns_update_kernel<S, kLast>), xcd_grid_halves<S>(update_tiles(S::BM)),
+        hipLaunchKernelGGL((ns_update_kernel<S, kLast>), dim3((unsigned)xcd_workgroups_halves<S>(update_tiles(S::BM))),
                            dim3(S::kThreads), 0, st, poly, hi[0], lo, hi[1], out, L.m, L.mp, L.n,
                            L.ld, mt, ct, (int)update_tiles(S::BM), 1.f / kGramScale, a - ident, kLast ? a - ident : a,
                            1.f / sx, L.tall, units + s);
