@@ -542,8 +542,8 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
 // X stays in registers in 32 bits (wave w holds column tiles w, w + 8, ...), its fp16 half for the
 // products in LDS, where A and B lie too; each wave computes an eighth of their sub-tiles. The
 // formats and scales are those above, with X itself in lo's place. Bound by latency: one matrix, five
-// steps (in brackets a launch a product), 64 x 512 30 us (80), 64 x 1024 55 (85), 128 x 256 43 (80),
-// 128 x 384 61 (86); 500 of 128 x 384 146 (415). Larger ones need more registers or LDS than a CU has.
+// steps (in brackets a launch a product), 64 x 512 31 us (80), 64 x 1024 55 (85), 128 x 256 43 (80),
+// 128 x 384 61 (86); 500 of 128 x 384 133 (415). Larger ones need more registers or LDS than a CU has.
 constexpr int kSmallWaves = 8;
 
 struct NsSmallArgs {
