@@ -224,9 +224,8 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int per = n_mtiles * n_ctiles;
-  int pos;
-  const int t = dw_tile(blockIdx.x, per, E, pos);
-  if (t < 0) return;
+  int pos, t;
+  if (!dw_tile(blockIdx.x, per, E, pos, t)) return;
   int begin, end;
   const int e = heavy_first(offsets, E, R, pos, lane, begin, end);
   if (e < 0) return;   // not reached: every expert has a position

@@ -51,7 +51,7 @@ constexpr bool kHalves = S::BN == 256 && S::kLdsBytes > 80 * 1024;
 template <class S>
 constexpr int xcd_tile_halves(int wg, int total, int& half) {
   const int per = (total + 7) >> 3, first = (wg & 7) * per;
-  const int mine = per < total - first ? per : total - first;   // tiles of this XCD
+  const int mine = std::min(per, total - first);   // tiles of this XCD
   int local = wg >> 3;
   half = -1;
   if constexpr (kHalves<S>) {
@@ -82,9 +82,8 @@ template <int BM>
 constexpr void block_rows(int n, int n_blocks, int i, int& first, int& rows) {
   constexpr int kUnit = BM % 64 == 0 ? 64 : BM;
   const int units = blocks_of<kUnit>(n), each = units / n_blocks, more = units % n_blocks;
-  first = kUnit * (i * each + (i < more ? i : more));
-  rows = kUnit * (each + (i < more ? 1 : 0));
-  if (rows > n - first) rows = n - first;
+  first = kUnit * (i * each + std::min(i, more));
+  rows = std::min(kUnit * (each + (i < more ? 1 : 0)), n - first);
 }
 
 // Tile v = b n_ctiles + .. of a deal of all blocks' column tiles, where block b is block in_expert of an
@@ -95,7 +94,7 @@ constexpr int kTileGroup = 4;
 constexpr void group_tile(int v, int b, int in_expert, int n_blocks, int n_ctiles, int& block,
                           int& ctile) {
   const int g0 = in_expert - in_expert % kTileGroup;
-  const int sz = kTileGroup < n_blocks - g0 ? kTileGroup : n_blocks - g0;
+  const int sz = std::min(kTileGroup, n_blocks - g0);
   const int at = v - (b - (in_expert - g0)) * n_ctiles;   // tile within the group
   block = g0 + at % sz;
   ctile = at / sz;
@@ -104,18 +103,19 @@ constexpr void group_tile(int v, int b, int in_expert, int n_blocks, int n_ctile
 // Tile t of one matrix, in bands of kTileGroup tile rows, column by column.
 constexpr void band_tile(int t, int n_mtiles, int n_ctiles, int& mtile, int& ctile) {
   const int m0 = t / (kTileGroup * n_ctiles) * kTileGroup;
-  const int sz = kTileGroup < n_mtiles - m0 ? kTileGroup : n_mtiles - m0, at = t - m0 * n_ctiles;
+  const int sz = std::min(kTileGroup, n_mtiles - m0), at = t - m0 * n_ctiles;
   mtile = m0 + at % sz;
   ctile = at / sz;
 }
 
-// Weight gradient: tile of workgroup `wg` among the `per` of one matrix (-1: none), and `pos`, the matrix's
-// position among the E, for a grid of dw_workgroups(per, E): each matrix's tiles in 8 runs, one an XCD.
-constexpr int dw_tile(int wg, int per, int E, int& pos) {
-  const int run = (per + 7) >> 3, local = wg >> 3;
-  const int t = (wg & 7) * run + local % run;
+// Weight gradient: tile t of workgroup `wg` among the `per` of one matrix, and `pos`, the matrix's position
+// among the E (false: no tile), for a grid of dw_workgroups(per, E): each matrix's tiles in 8 runs, one
+// an XCD.
+constexpr bool dw_tile(unsigned wg, int per, int E, int& pos, int& t) {
+  const int run = (per + 7) >> 3, local = (int)(wg >> 3);
+  t = (int)(wg & 7) * run + local % run;
   pos = local / run;
-  return pos < E && t < per ? t : -1;
+  return pos < E && t < per;
 }
 inline int64_t dw_workgroups(int64_t per, int64_t E) { return 8 * E * ceil_div(per, 8); }
 

@@ -208,9 +208,8 @@ void dw_deal(int64_t R, int E, int N, int K, bool bf16) {
     expect(wgs * S::kThreads < kMaxThreads, "threads", R, E, N, K);
     std::vector<unsigned char> seen((size_t)per * E, 0);
     for (int64_t wg = 0; wg < wgs; ++wg) {
-      int pos = -1, mt = -1, ct = -1;
-      const int t = beam::dw_tile((int)wg, per, E, pos);
-      if (t < 0) continue;
+      int pos = -1, t = -1, mt = -1, ct = -1;
+      if (!beam::dw_tile((unsigned)wg, per, E, pos, t)) continue;
       beam::band_tile(t, n_mtiles, n_ctiles, mt, ct);
       const bool in = pos >= 0 && pos < E && mt >= 0 && mt < n_mtiles && ct >= 0 && ct < n_ctiles;
       expect(in && !seen[((size_t)pos * n_mtiles + mt) * n_ctiles + ct], "tile dealt once", E, N, K, wg);
