@@ -335,6 +335,126 @@ BEAM_API beam_status_t beam_moe_orthogonalise(const void* g, int32_t g_dtype, vo
                                               void* stream);
 BEAM_API size_t beam_moe_orthogonalise_workspace_bytes(int64_t n_mats, int32_t rows, int32_t cols);
 
+/* Gated feed-forward products grouped by expert, rows and offsets as for beam_moe_grouped_mm (a dense layer:
+ * E = 1, offsets {0, R}): both projections, the activation and the product in one launch, and the gradient
+ * through them behind the down projection. With the grouped products they are an expert's training step:
+ *   h, gu = gated_mm(x, w_gate_up);  y = grouped_mm(h, w_down);  the rows' routing weights scale y
+ *   d_gu, h', d_row_scale = gated_mm_backward(dy, w_down, gu, row_scale)
+ *   dx = grouped_mm_dx(d_gu, w_gate_up);  dw_gate_up = grouped_mm_dw(d_gu, x);  dw_down = grouped_mm_dw(dy, h')
+ * Forward, products in FP32:
+ *   (g | u) = x[r] . w_gate_up[e]^T,  h[r] = bf16(silu(g) u)
+ *   x          [R][K] bf16;  w_gate_up [E][2 F][K] bf16 (gate rows, then up rows)
+ *   h          [R][F] bf16 out
+ *   gu         [R][2 F] bf16 out: g, then u, rounded; NULL: not kept
+ *   round_products  != 0: h is taken from the rounded g and u, as the block's own forward does (the values that
+ *              served a recorded route); 0: from the FP32 ones
+ * Gradient, in FP32 from the stored g and u, roundings passed through as the identity, s = row_scale[r]:
+ *   dh = dy[r] . w_down[e],  sig = 1 / (1 + e^-g)
+ *   d_gu[r] = bf16(s dh u sig (1 + g (1 - sig)) | s dh silu(g)),  h[r] = bf16(s silu(g) u)
+ *   d_row_scale[r] = sum over F of dh silu(g) u
+ *   dy         [R][H] bf16: gradient of the down projection's output, unscaled (of row_scale[r] y[r])
+ *   w_down     [E][H][F] bf16
+ *   row_scale  [R] fp32, or NULL: s = 1, d_row_scale NULL too and no workspace
+ *   d_gu       [R][2 F], h [R][F] bf16 out, d_row_scale [R] fp32 out
+ *   workspace  with row_scale: at least beam_moe_gated_mm_backward_workspace_bytes(R, F)
+ * Rows of no expert are not read, and their outputs are left as they were. R = 0 is a no-op. g of a size where
+ * e^-g overflows gives the limits (sig 0 or 1). Equal calls give equal bits.
+ * Limits: F % 8 == 0, K % 8 == 0, H % 8 == 0, each <= 2^20, 2 F * K < 2^30, F * H < 2^30, E <= 4096, R < 2^31, and
+ * launches of fewer than 2^32 threads. */
+BEAM_API beam_status_t beam_moe_gated_mm(const void* x, const void* w_gate_up, const int32_t* offsets,
+                                         void* h, void* gu, int64_t R, int32_t E, int32_t F, int32_t K,
+                                         int32_t round_products, void* stream);
+BEAM_API beam_status_t beam_moe_gated_mm_backward(const void* dy, const void* w_down, const void* gu,
+                                                  const int32_t* offsets, const float* row_scale,
+                                                  void* d_gu, void* h, float* d_row_scale, int64_t R,
+                                                  int32_t E, int32_t F, int32_t H, void* workspace,
+                                                  size_t workspace_bytes, void* stream);
+BEAM_API size_t beam_moe_gated_mm_backward_workspace_bytes(int64_t R, int32_t F);
+
+/* Loss of the output head (softmax cross entropy over a large vocabulary) without its logits in memory, and
+ * the gradient; x is the last boundary's x_next, so dx is beam_residual_boundary_backward's d_x_next:
+ *   z[t][v] = x[t] . w[v], with softcap c > 0: c tanh(z / c) ([H] §专家混合 gives Beam's final logits c = 30)
+ *   lse[t] = log sum_v e^z,  loss[t] = lse[t] - z[t][targets[t]]      (-loss: the token's log-probability)
+ *   dz = d_loss[t] (e^(z - lse[t]) - [v = targets[t]]) (1 - (z / c)^2),  dx = dz w,  dw = dz^T x
+ *   x          [T][H] bf16;  w [V][H] bf16
+ *   targets    [T] int32; one outside [0, V) has no loss and no gradient (its loss is 0, lse is still given)
+ *   loss, lse  [T] fp32 out (lse is what the gradient takes)
+ *   d_loss     [T] fp32: the gradient of each token's loss (1 / T for a mean)
+ *   dx         [T][H] bf16 out;  dw [V][H] dw_dtype out (BEAM_BF16 or BEAM_F32)
+ *   softcap    0: none; else 1/16 to 1024
+ *   workspace  at least beam_head_loss_workspace_bytes, beam_head_loss_backward_workspace_bytes(T, V, H)
+ * Logits are FP32 sums of exact products; e^z, their sums and dz are FP32. dz is rounded to bf16 for the two
+ * products, whose sums are FP32 again: dx and dw carry that rounding (2^-9 of each of their terms), an FP32 dw
+ * too. The gradient works on pieces of the vocabulary, at most 512 MiB (or 512 columns) of dz at a time; the
+ * loss keeps 8 bytes for each token and 64 to 256 columns. T = 0: no-ops, but dw is set to zero (the other
+ * pointers may then be NULL). Equal calls give equal bits.
+ * Limits: H % 8 == 0, H <= 2^20, V <= 2^23, T < 2^31, and launches of fewer than 2^32 threads. */
+BEAM_API beam_status_t beam_head_loss(const void* x, const void* w, const int32_t* targets, float* loss,
+                                      float* lse, int64_t T, int64_t V, int32_t H, float softcap,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+BEAM_API size_t beam_head_loss_workspace_bytes(int64_t T, int64_t V, int32_t H);
+BEAM_API beam_status_t beam_head_loss_backward(const void* x, const void* w, const int32_t* targets,
+                                               const float* lse, const float* d_loss, void* dx, void* dw,
+                                               int32_t dw_dtype, int64_t T, int64_t V, int32_t H,
+                                               float softcap, void* workspace, size_t workspace_bytes,
+                                               void* stream);
+BEAM_API size_t beam_head_loss_backward_workspace_bytes(int64_t T, int64_t V, int32_t H);
+
+/* AdamW step over many tensors in place: what the orthogonalised update is not for (norms, router, embedding,
+ * head).
+ *   g = grad * grad_scale,  m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   param = param (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * One tensor of the call, `count` values (0: skipped), each array contiguous:
+ *   param      param_dtype (BEAM_F32 or BEAM_BF16), updated
+ *   grad       grad_dtype (BEAM_F32 or BEAM_BF16)
+ *   m, v       the states, state_dtype, updated: BEAM_F32, or BEAM_FP8_E4M3: uint8 E4M3FN codes of m and of
+ *              sqrt(v), each times the scale of its 256 values
+ *   m_scale, v_scale  [ceil(count / 256)] fp32, updated (BEAM_FP8_E4M3 only; 4-byte aligned): a block's largest
+ *              magnitude (at least 2^-100) / 448. Zero codes with any scale start a run.
+ *   copy       bf16 out: the updated FP32 weights rounded to nearest even, or NULL (for all tensors or none)
+ * The call's numbers (a host struct, read before the call returns):
+ *   step       t >= 1, or step_on_device: a device int32 (4-byte aligned) read by the launches instead
+ *   lr         or lr_on_device: a device fp32 read instead
+ *   grad_scale device fp32, or NULL: 1. If it is infinite or NaN the call changes nothing (a step whose
+ *              gradients overflowed).
+ *   stochastic != 0: bf16 weights and 8-bit states are rounded up or down at random, in proportion, instead of
+ *              to nearest; the bits are a hash of seed, step and the value's number (tensors numbered through in
+ *              the call's order, each from a multiple of 256), so equal calls give equal bits. Rounding to
+ *              nearest loses changes under half a step of the type (2^-9 of a bf16 weight, 3 to 6% of an 8-bit
+ *              state a step).
+ * A state, its root and their rounding are correctly rounded FP32 operations without fused ones. 8-bit roots
+ * above zero stay above zero (at least 2^-9 of the scale). A gradient that is not finite makes its value's
+ * state and weight so, and with 8-bit states its block's.
+ * beam_moe_adamw checks each tensor by itself; beam_moe_adamw_check, for a list made once, also that no two of
+ * the list's arrays overlap (gradients may share memory).
+ * Limits: 0 <= beta < 1, 1e-30 <= eps <= 1e30, count under 2^36, fewer than 2^39 values in all. No workspace;
+ * n = 0 is a no-op. */
+typedef struct beam_adamw_tensor {
+  void* param;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  void* copy;
+  int64_t count;
+} beam_adamw_tensor;
+typedef struct beam_adamw_cfg {
+  double lr, beta1, beta2, eps, weight_decay;
+  int32_t step;
+  int32_t stochastic;
+  uint32_t seed;
+  uint32_t reserved;
+  const int32_t* step_on_device;
+  const float* lr_on_device;
+  const float* grad_scale;
+} beam_adamw_cfg;
+BEAM_API beam_status_t beam_moe_adamw(const beam_adamw_tensor* tensors, int32_t n, int32_t param_dtype,
+                                      int32_t grad_dtype, int32_t state_dtype, const beam_adamw_cfg* cfg,
+                                      void* stream);
+BEAM_API beam_status_t beam_moe_adamw_check(const beam_adamw_tensor* tensors, int32_t n,
+                                            int32_t param_dtype, int32_t grad_dtype, int32_t state_dtype);
+
 /* Dynamic FP8 E4M3 quantisation of bf16 rows, the activation step of the FP8 experts (dynamic FP8
  * checkpoints: [S] §Highlights, §BF16, NVFP4 and FP8 Model Support).
  *   src    [rows][cols] bf16 (device), cols % 8 == 0

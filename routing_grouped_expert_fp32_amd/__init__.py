@@ -26,7 +26,9 @@ __all__ = [
     "workspace_view", "WS_REGIONS", "convert", "dense_workspace_region", "fp8_dot_tiles",
     "forward_noalloc", "grouped_mm", "grouped_mm_dx", "grouped_mm_dw",
     "residual_boundary_backward", "residual_boundary_backward_workspace_bytes", "orthogonalise",
-    "orthogonalise_workspace_bytes",
+    "orthogonalise_workspace_bytes", "gated_mm", "gated_mm_backward",
+    "gated_mm_backward_workspace_bytes", "head_loss", "head_loss_workspace_bytes",
+    "head_loss_backward", "head_loss_backward_workspace_bytes", "AdamWPlan", "adamw_plan", "adamw",
 ]
 
 BEAM_F32, BEAM_BF16, BEAM_FP8_E4M3 = 0, 1, 2
@@ -57,6 +59,18 @@ def make_cfg(hidden=5120, n_experts=256, n_groups=8, topk_groups=4, topk=8, d_ff
              routed_scale=2.5, x_dtype=BEAM_BF16, w_dtype=BEAM_BF16, out_dtype=BEAM_F32) -> Cfg:
     return Cfg(hidden, n_experts, n_groups, topk_groups, topk, d_ff, routed_scale, x_dtype,
                w_dtype, out_dtype)
+
+
+class _AdamWTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "m", "v", "m_scale", "v_scale", "copy")]
+    _fields_ += [("count", ctypes.c_int64)]
+
+
+class _AdamWCfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")]
+    _fields_ += [("step", ctypes.c_int32), ("stochastic", ctypes.c_int32), ("seed", ctypes.c_uint32),
+                 ("reserved", ctypes.c_uint32), ("step_on_device", ctypes.c_void_p),
+                 ("lr_on_device", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p)]
 
 
 _LIB = None
@@ -135,6 +149,26 @@ def lib() -> ctypes.CDLL:
         L.beam_moe_orthogonalise.restype = i32
         L.beam_moe_orthogonalise_workspace_bytes.argtypes = [i64, i32, i32]
         L.beam_moe_orthogonalise_workspace_bytes.restype = sz
+        L.beam_moe_gated_mm.argtypes = [vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, vp]
+        L.beam_moe_gated_mm.restype = i32
+        L.beam_moe_gated_mm_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, i32,
+                                                 vp, sz, vp]
+        L.beam_moe_gated_mm_backward.restype = i32
+        L.beam_moe_gated_mm_backward_workspace_bytes.argtypes = [i64, i32]
+        L.beam_moe_gated_mm_backward_workspace_bytes.restype = sz
+        L.beam_head_loss.argtypes = [vp, vp, vp, vp, vp, i64, i64, i32, f32, vp, sz, vp]
+        L.beam_head_loss.restype = i32
+        L.beam_head_loss_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i64, i64, i32, f32, vp,
+                                              sz, vp]
+        L.beam_head_loss_backward.restype = i32
+        for name in ("beam_head_loss_workspace_bytes", "beam_head_loss_backward_workspace_bytes"):
+            getattr(L, name).argtypes = [i64, i64, i32]
+            getattr(L, name).restype = sz
+        tensors = ctypes.POINTER(_AdamWTensor)
+        L.beam_moe_adamw.argtypes = [tensors, i32, i32, i32, i32, ctypes.POINTER(_AdamWCfg), vp]
+        L.beam_moe_adamw.restype = i32
+        L.beam_moe_adamw_check.argtypes = [tensors, i32, i32, i32, i32]
+        L.beam_moe_adamw_check.restype = i32
         L.beam_moe_convert.argtypes = [vp, i64, i32, vp, vp]
         L.beam_moe_convert.restype = i32
         _LIB = L
@@ -542,6 +576,254 @@ def orthogonalise(g, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: floa
     if rc != 0:
         raise BeamError(rc, "beam_moe_orthogonalise")
     return out
+
+
+def _aligned_offsets(offsets):
+    """The offsets at an address that the C ABI takes: a view of a longer table may lie between."""
+    return offsets.clone() if offsets.data_ptr() & 15 else offsets
+
+
+def gated_mm(x, w_gate_up, offsets, keep=False, round_products=False, h=None, gu=None, stream=None):
+    """beam_moe_gated_mm: returns (h, gu), h [R][F] = silu(g) * u of the rows offsets[e] ..
+    offsets[e + 1] of expert e and gu [R][2F] their products g | u (bf16), which the backward takes; gu is
+    None unless `keep` or a tensor for it is given. x [R][K] and w_gate_up [E][2F][K] bf16, offsets
+    [E + 1] int32. round_products: h from the rounded products, as the block's forward takes it. Rows
+    outside the offsets are left as they were (undefined in new tensors)."""
+    (R, K), (E, F2, _) = x.shape, w_gate_up.shape
+    F, bf = F2 // 2, torch.bfloat16
+    _check_tensor("x", x, (R, K), bf)
+    _check_tensor("w_gate_up", w_gate_up, (E, 2 * F, K), bf)
+    _check_tensor("offsets", offsets, (E + 1,), torch.int32)
+    if h is not None:
+        _check_tensor("h", h, (R, F), bf)
+    if gu is not None:
+        _check_tensor("gu", gu, (R, 2 * F), bf)
+    ctx, st = _on(_device_of(x, w_gate_up, offsets, h, gu), stream)
+    with ctx:
+        if h is None:
+            h = x.new_empty((R, F))
+        if gu is None and keep:
+            gu = x.new_empty((R, 2 * F))
+        offsets = _aligned_offsets(offsets)
+        rc = lib().beam_moe_gated_mm(x.data_ptr(), w_gate_up.data_ptr(), offsets.data_ptr(), h.data_ptr(),
+                                     None if gu is None else gu.data_ptr(), R, E, F, K,
+                                     int(bool(round_products)), st)
+    if rc != 0:
+        raise BeamError(rc, "beam_moe_gated_mm")
+    return h, gu
+
+
+def gated_mm_backward_workspace_bytes(R: int, F: int) -> int:
+    return int(lib().beam_moe_gated_mm_backward_workspace_bytes(R, F))
+
+
+def gated_mm_backward(dy, w_down, gu, offsets, row_scale=None, d_gu=None, h=None, d_row_scale=None,
+                      workspace=None, stream=None):
+    """beam_moe_gated_mm_backward: returns (d_gu, h, d_row_scale) from dy [R][H], the gradient of
+    row_scale[r] * (h[r] . w_down[e]^T), w_down [E][H][F] and the gu that gated_mm kept. h [R][F] is
+    the activation times the row's scale, so the weight gradients are grouped_mm_dw(dy, h, offsets) and
+    grouped_mm_dw(d_gu, x, offsets). Without row_scale (fp32 [R]) the scales are 1 and d_row_scale None."""
+    (R, H), (E, _, F) = dy.shape, w_down.shape
+    bf, f32 = torch.bfloat16, torch.float32
+    _check_tensor("dy", dy, (R, H), bf)
+    _check_tensor("w_down", w_down, (E, H, F), bf)
+    _check_tensor("gu", gu, (R, 2 * F), bf)
+    _check_tensor("offsets", offsets, (E + 1,), torch.int32)
+    if row_scale is None and d_row_scale is not None:
+        raise ValueError("d_row_scale: there is no row_scale")
+    for name, t, shape, dt in (("row_scale", row_scale, (R,), f32), ("d_gu", d_gu, (R, 2 * F), bf),
+                               ("h", h, (R, F), bf), ("d_row_scale", d_row_scale, (R,), f32)):
+        if t is not None:
+            _check_tensor(name, t, shape, dt)
+    ctx, st = _on(_device_of(dy, w_down, gu, offsets, row_scale, d_gu, h, d_row_scale, workspace), stream)
+    with ctx:
+        d_gu = torch.empty_like(gu) if d_gu is None else d_gu
+        h = gu.new_empty((R, F)) if h is None else h
+        ws, nbytes = None, 0
+        if row_scale is not None:
+            d_row_scale = torch.empty_like(row_scale) if d_row_scale is None else d_row_scale
+            if workspace is None:
+                need = gated_mm_backward_workspace_bytes(R, F)
+                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dy.device)
+            ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        offsets = _aligned_offsets(offsets)
+        rc = lib().beam_moe_gated_mm_backward(
+            dy.data_ptr(), w_down.data_ptr(), gu.data_ptr(), offsets.data_ptr(),
+            None if row_scale is None else row_scale.data_ptr(), d_gu.data_ptr(), h.data_ptr(),
+            None if row_scale is None else d_row_scale.data_ptr(), R, E, F, H, ws, nbytes, st)
+    if rc != 0:
+        raise BeamError(rc, "beam_moe_gated_mm_backward")
+    return d_gu, h, d_row_scale
+
+
+def head_loss_workspace_bytes(T: int, V: int, H: int) -> int:
+    return int(lib().beam_head_loss_workspace_bytes(T, V, H))
+
+
+def head_loss(x, w, targets, softcap: float = 0.0, loss=None, lse=None, workspace=None, stream=None):
+    """beam_head_loss: returns (loss, lse), fp32 [T]: the cross entropy of each token's target under the
+    logits x . w^T (capped as softcap * tanh(z / softcap) if softcap > 0), which are not kept, and their
+    log-sum-exp, which head_loss_backward takes. x [T][H] and w [V][H] bf16, targets [T] int32; a target
+    outside [0, V) has no loss."""
+    (T, H), V = x.shape, w.shape[0]
+    bf, f32 = torch.bfloat16, torch.float32
+    _check_tensor("x", x, (T, H), bf)
+    _check_tensor("w", w, (V, H), bf)
+    _check_tensor("targets", targets, (T,), torch.int32)
+    for name, t in (("loss", loss), ("lse", lse)):
+        if t is not None:
+            _check_tensor(name, t, (T,), f32)
+    ctx, st = _on(_device_of(x, w, targets, loss, lse, workspace), stream)
+    with ctx:
+        loss = x.new_empty((T,), dtype=f32) if loss is None else loss
+        lse = x.new_empty((T,), dtype=f32) if lse is None else lse
+        if workspace is None:
+            need = head_loss_workspace_bytes(T, V, H)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+        rc = lib().beam_head_loss(x.data_ptr(), w.data_ptr(), targets.data_ptr(), loss.data_ptr(),
+                                  lse.data_ptr(), T, V, H, float(softcap), workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), st)
+    if rc != 0:
+        raise BeamError(rc, "beam_head_loss")
+    return loss, lse
+
+
+def head_loss_backward_workspace_bytes(T: int, V: int, H: int) -> int:
+    return int(lib().beam_head_loss_backward_workspace_bytes(T, V, H))
+
+
+def head_loss_backward(x, w, targets, lse, d_loss, softcap: float = 0.0, dx=None, dw=None,
+                       dw_dtype=BEAM_BF16, workspace=None, stream=None):
+    """beam_head_loss_backward: returns (dx, dw), the gradients of sum(d_loss * loss) of head_loss's call
+    with these x, w, targets and softcap that gave lse; d_loss fp32 [T]. dx [T][H] is bf16, dw [V][H] bf16
+    or (dw_dtype=BEAM_F32) fp32."""
+    if dw_dtype not in (BEAM_F32, BEAM_BF16):
+        raise BeamError(4, "beam_head_loss_backward")   # BEAM_ERR_DTYPE
+    (T, H), V = x.shape, w.shape[0]
+    bf, f32 = torch.bfloat16, torch.float32
+    wdt = bf if dw_dtype == BEAM_BF16 else f32
+    _check_tensor("x", x, (T, H), bf)
+    _check_tensor("w", w, (V, H), bf)
+    _check_tensor("targets", targets, (T,), torch.int32)
+    _check_tensor("lse", lse, (T,), f32)
+    _check_tensor("d_loss", d_loss, (T,), f32)
+    if dx is not None:
+        _check_tensor("dx", dx, (T, H), bf)
+    if dw is not None:
+        _check_tensor("dw", dw, (V, H), wdt)
+    ctx, st = _on(_device_of(x, w, targets, lse, d_loss, dx, dw, workspace), stream)
+    with ctx:
+        dx = torch.empty_like(x) if dx is None else dx
+        dw = w.new_empty((V, H), dtype=wdt) if dw is None else dw
+        if workspace is None:
+            need = head_loss_backward_workspace_bytes(T, V, H)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+        rc = lib().beam_head_loss_backward(
+            x.data_ptr(), w.data_ptr(), targets.data_ptr(), lse.data_ptr(), d_loss.data_ptr(),
+            dx.data_ptr(), dw.data_ptr(), dw_dtype, T, V, H, float(softcap), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), st)
+    if rc != 0:
+        raise BeamError(rc, "beam_head_loss_backward")
+    return dx, dw
+
+
+class AdamWPlan:
+    """The tensors of an AdamW step (adamw_plan), which it holds, and their table for the C ABI."""
+    __slots__ = ("tensors", "table", "grads", "dtypes", "device")
+
+
+def _adamw_grads(plan, grads):
+    if len(grads) != len(plan.grads):
+        raise ValueError(f"grads: expected {len(plan.grads)} tensors, got {len(grads)}")
+    gdt = plan.grads[0].dtype if plan.grads else None
+    for i, (g, was) in enumerate(zip(grads, plan.grads)):
+        _check_tensor(f"grads[{i}]", g, was.shape, gdt)
+        if g.get_device() != plan.device or not g.is_contiguous():
+            raise ValueError(f"grads[{i}]: must be contiguous on the plan's device")
+
+
+def adamw_plan(params, grads, m, v, m_scales=None, v_scales=None, copies=None) -> AdamWPlan:
+    """The plan of an AdamW step over lists of contiguous tensors on one device, made once: params (all
+    fp32 or all bf16), grads (all fp32 or all bf16), and states m, v of the params' shapes, fp32, or
+    float8_e4m3fn (uint8 codes) with m_scales, v_scales: fp32 of ceil(count / 256) values. copies: bf16
+    tensors that take the updated fp32 weights. The plan keeps the tensors and their addresses: make
+    another if their storage is replaced. No two tensors may overlap (beam_moe_adamw_check)."""
+    params, grads, m, v = list(params), list(grads), list(m), list(v)
+    n, f32, bf = len(params), torch.float32, torch.bfloat16
+    eight = n > 0 and m[:1] != [] and m[0].dtype != f32
+    lists = [("grads", grads), ("m", m), ("v", v)]
+    if eight != (m_scales is not None) or eight != (v_scales is not None):
+        raise ValueError("m_scales, v_scales: given with 8-bit states, and only with them")
+    scales = [list(m_scales), list(v_scales)] if eight else [[None] * n, [None] * n]
+    lists += [("m_scales", scales[0]), ("v_scales", scales[1])]
+    copies_ = [None] * n if copies is None else list(copies)
+    for name, ts in lists + [("copies", copies_)]:
+        if len(ts) != n:
+            raise ValueError(f"{name}: expected {n} tensors, got {len(ts)}")
+    sdt = (torch.float8_e4m3fn, torch.uint8) if eight else (f32,)
+    pdt, gdt = (params[0].dtype, grads[0].dtype) if n else (f32, f32)
+    for dt, name in ((pdt, "params"), (gdt, "grads")):
+        if dt not in (f32, bf):
+            raise ValueError(f"{name}: expected torch.float32 or torch.bfloat16, got {dt}")
+    table = (_AdamWTensor * max(n, 1))()
+    for i in range(n):
+        p, shape, blocks = params[i], params[i].shape, ((params[i].numel() + 255) // 256,)
+        _check_tensor(f"params[{i}]", p, shape, pdt)
+        _check_tensor(f"grads[{i}]", grads[i], shape, gdt)
+        _check_tensor(f"m[{i}]", m[i], shape, *sdt)
+        _check_tensor(f"v[{i}]", v[i], shape, *sdt)
+        for name, ts in (("m_scales", scales[0]), ("v_scales", scales[1])):
+            if ts[i] is not None:
+                _check_tensor(f"{name}[{i}]", ts[i], blocks, f32)
+        if copies_[i] is not None:
+            _check_tensor(f"copies[{i}]", copies_[i], shape, bf)
+        row = (p, grads[i], m[i], v[i], scales[0][i], scales[1][i], copies_[i])
+        table[i] = _AdamWTensor(*[None if t is None else t.data_ptr() for t in row], p.numel())
+    plan = AdamWPlan()
+    plan.tensors = (params, m, v, scales, copies_)
+    plan.grads, plan.table = grads, table
+    plan.dtypes = (_DT_CODE[pdt], _DT_CODE[gdt], BEAM_FP8_E4M3 if eight else BEAM_F32)
+    plan.device = _device_of(*params, *grads, *m, *v, *scales[0], *scales[1], *copies_)
+    rc = lib().beam_moe_adamw_check(table, n, *plan.dtypes)
+    if rc != 0:
+        raise BeamError(rc, "beam_moe_adamw_check")
+    return plan
+
+
+def adamw(plan: AdamWPlan, step, lr, betas=(0.9, 0.95), eps: float = 1e-8, weight_decay: float = 0.0,
+          grad_scale=None, seed=None, grads=None, stream=None) -> None:
+    """beam_moe_adamw: one step of the plan's tensors, in place. step: t >= 1, or a device int32 of one
+    value; lr: a number, or a device fp32 of one value (for captured steps). grad_scale: a device fp32 of
+    one value that the gradients are multiplied by; the step is left out if it is not finite. seed: bf16
+    weights and 8-bit states are rounded stochastically. grads: this step's, instead of the plan's."""
+    if plan.device is None:
+        return
+    scalars = []
+    for name, t, dt in (("step", step, torch.int32), ("lr", lr, torch.float32),
+                        ("grad_scale", grad_scale, torch.float32)):
+        if isinstance(t, torch.Tensor):
+            if t.numel() != 1 or t.dtype != dt or t.get_device() != plan.device:
+                raise ValueError(f"{name}: expected one {dt} on the plan's device")
+            scalars.append(t.data_ptr())
+        else:
+            scalars.append(None)
+    if grad_scale is not None and scalars[2] is None:
+        raise ValueError("grad_scale: expected a tensor")
+    cfg = _AdamWCfg(0.0 if scalars[1] else float(lr), float(betas[0]), float(betas[1]), float(eps),
+                    float(weight_decay), 0 if scalars[0] else int(step), int(seed is not None),
+                    0 if seed is None else int(seed) & 0xFFFFFFFF, 0, scalars[0], scalars[1], scalars[2])
+    n, table = len(plan.grads), plan.table
+    if grads is not None:
+        grads = list(grads)
+        _adamw_grads(plan, grads)
+        table = type(table).from_buffer_copy(table)
+        for i, g in enumerate(grads):
+            table[i].grad = g.data_ptr()
+    ctx, st = _on(plan.device, stream)
+    with ctx:
+        rc = lib().beam_moe_adamw(table, n, *plan.dtypes, ctypes.byref(cfg), st)
+    if rc != 0:
+        raise BeamError(rc, "beam_moe_adamw")
 
 
 WS_REGIONS = {"expert_off": 0, "sorted_slot": 1, "h": 2, "hq": 3, "hs": 4, "xq": 5, "xs": 6,

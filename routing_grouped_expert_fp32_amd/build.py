@@ -16,7 +16,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbeam_moe.so")
 SOURCES = ["api.cpp", "host_rules.cpp", "scratch.hip", "router.hip", "align.hip",
            "gemm_grouped.hip", "gemm_f32.hip", "fp8.hip", "combine.hip", "boundary.hip",
-           "api_train.cpp", "train_rules.cpp", "grouped_mm.hip", "boundary_bwd.hip", "orthogonalise.hip"]
+           "api_train.cpp", "train_rules.cpp", "grouped_mm.hip", "boundary_bwd.hip", "orthogonalise.hip",
+           "api_step.cpp", "step_rules.cpp", "gated.hip", "head_loss.hip", "adamw.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 FLAGS = [

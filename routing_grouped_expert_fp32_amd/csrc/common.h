@@ -189,4 +189,50 @@ bool ns_grid_fits(int64_t n_mats, int rows, int cols);
 hipError_t launch_orthogonalise(const void* g, bool g_bf16, uint16_t* out, int n_mats, int rows,
                                 int cols, int steps, const float* coeffs, float eps, char* ws,
                                 hipStream_t st);
+
+// ---- operators that close a training step ----
+// Gated products: h [R][F], gu [R][2 F] (nullable) of x [R][K] and w [E][2 F][K]; and the gradient through
+// them, d_gu [R][2 F] and h [R][F] of dy [R][H] and w [E][H][F], with the rows' scales their gradient
+// d_scale [R] too (parts: gated_scale_parts(F) x R). `rounded`: g and u to bf16 before the activation.
+hipError_t launch_gated(const void* x, const void* w, const int32_t* offsets, void* h, void* gu, int R, int E,
+                        int F, int K, bool rounded, hipStream_t st);
+hipError_t launch_gated_bwd(const void* dy, const void* w, const void* gu, const int32_t* offsets,
+                            const float* scale, void* d_gu, void* h, float* d_scale, float* parts, int R, int E,
+                            int F, int H, hipStream_t st);
+
+// Loss of the output head: logits z = x w^T (T x V, contraction H), cap > 0: cap tanh(z / cap).
+struct HeadArgs {
+  const uint16_t* x;         // [T][H]
+  const uint16_t* w;         // [V][H]
+  const int32_t* targets;    // [T]; outside [0, V): no loss
+  int64_t T, V;
+  int H;
+  float cap;
+};
+hipError_t launch_head_loss(const HeadArgs& a, float* loss, float* lse, char* ws, hipStream_t st);
+hipError_t launch_head_loss_bwd(const HeadArgs& a, const float* lse, const float* d_loss, uint16_t* dx, void* dw,
+                                bool dw_bf16, char* ws, hipStream_t st);
+
+// One tensor of an AdamW step (layouts: include/beam_moe.h), and the numbers that all share.
+struct AdamwTensor {
+  void* param;
+  const void* grad;
+  void *m, *v;
+  float *m_scale, *v_scale;
+  void* copy;
+  int64_t count;
+};
+struct AdamwScalars {
+  float beta1, rest1, beta2, rest2;   // rest: 1 - beta
+  float lr, weight_decay, decay;      // decay: 1 - lr weight_decay
+  float eps;
+  float correction, root_scale;       // 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
+  float log_beta1, log_beta2;
+  uint32_t key;                       // of the random bits; with `step`, before the step is mixed in
+  const int32_t* step;                // t on the device (nullable)
+  const float* lr_now;                // lr on the device (nullable)
+  const float* grad_scale;            // nullable: 1
+};
+hipError_t launch_adamw(const AdamwTensor* tensors, int n, bool p_bf16, bool g_bf16, bool q8, bool copy,
+                        bool noise, const AdamwScalars& s, hipStream_t st);
 }  // namespace beam

@@ -69,6 +69,11 @@ struct OperandLoader {
   int kofs;   // row operands: first k of this lane's chunk within a stage
 
   __device__ __forceinline__ void init(const TileOperand& o, int wave, int lane) {
+    init(o, wave, lane, [](int row) { return row; });
+  }
+  // row operands: row r of the tile is stored row at(r) from `base` (op.rows: one past the last of them)
+  template <class At>
+  __device__ __forceinline__ void init(const TileOperand& o, int wave, int lane, At&& at) {
     op = o;
     const int slot = lane % kRowChunks, lr = lane / kRowChunks;
     kofs = 8 * (slot ^ (lr & 7));
@@ -79,7 +84,7 @@ struct OperandLoader {
         const int f = column_swizzle<ROWS>(row & 3, (row >> 3) & 1);
         voff[q] = (uint32_t)(row * op.ld + (slot ^ (f << 1)) * 16);
       } else {
-        voff[q] = (uint32_t)(row * op.ld + kofs * 2);
+        voff[q] = (uint32_t)(at(row) * op.ld + kofs * 2);
       }
     }
   }

@@ -1,0 +1,94 @@
+// Host-side rules of the operators that close a training step (gfx950): tiles, launch and workspace sizes
+// of the gated products, of the head's loss and of the AdamW step. Plain C++, as train_rules.h.
+#pragma once
+
+#include "train_rules.h"
+
+namespace beam {
+
+// ---- gated products grouped by expert ----
+// A tile's columns are half gate, half up, in sub-tiles of 16 in turn, so each wave needs an even
+// number of them: every tile of the grouped products but the 32 x 64 one. The products' rule, over the
+// 2 F rows of the weights.
+template <class S>
+constexpr int kGatedCols = S::BN / 2;
+template <class F>
+void with_gated_tile(int64_t R, int64_t E, int64_t Fw, int64_t K, bool keep, F&& f) {
+  const RowsCall call(R, E, 2 * Fw, K, R * (Fw * (keep ? 6e-6 : 2e-6)));
+  with_least([&](auto s) { return call.us(s); }, f, TileStream{}, Tile64{}, TilePair{}, Tile128{}, Tile192{},
+             Tile256Deep{}, Tile320{});
+}
+
+// The gradient's tiles: F columns, contraction over the hidden width; 10 bytes a value beside dy.
+template <class F>
+void with_gated_bwd_tile(int64_t R, int64_t E, int64_t Fw, int64_t H, F&& f) {
+  const RowsCall call(R, E, Fw, H, R * (Fw * 10e-6));
+  with_least([&](auto s) { return call.us(s); }, f, TileStream{}, TileLone{}, Tile64{}, TilePair{}, Tile128{},
+             Tile192{}, Tile256Deep{}, Tile320{});
+}
+// Partial sums of the scales' gradient: one for the columns of a wave, or of a wave of its half tile.
+template <class S>
+constexpr int kScaleCols = kHalves<S> ? S::FN * 8 : S::FN * 16;
+constexpr int kLeastScaleCols = 16;
+inline int64_t gated_scale_parts(int64_t Fw) { return ceil_div(Fw, kLeastScaleCols); }
+
+// ---- loss of the output head ----
+// Logits: the grouped products' rule for one expert of V columns, by tile shape; `store`: their gradient is
+// stored, in bf16.
+template <class F>
+void with_head_tile(int64_t T, int64_t V, int64_t H, bool store, F&& f) {
+  const RowsCall call(T, 1, V, H, store ? T * (V * 2e-6) : 0.0);
+  with_least([&](auto s) { return call.us(s); }, f, TileStream{}, Tile64{}, TilePair{}, Tile128{}, Tile192{},
+             Tile256Deep{}, Tile320{});
+}
+// Column slots of a row's partial sums: one a tile, two where a tile may be split.
+template <class S>
+int64_t head_slots(int64_t V) {
+  return ceil_div(V, S::BN) * (kHalves<S> ? 2 : 1);
+}
+
+// Gradient of x: tiles of T x H, the contraction over a piece of the vocabulary cut into `parts` runs of
+// `kp` values (whole stages), each with FP32 sums of its own that are added in order. Per tile shape, us: its
+// ends and a stage where the GPU is full.
+struct HeadDxPlan {
+  int side;       // tile: 256, 128 or 64 square, 32: 32 x 128
+  int parts;
+  int64_t kp;
+};
+using DxTile256 = TileShape<256, 256, 2, 4, 2, 2>;
+using DxTile128 = TileShape<128, 128, 2, 2, 2, 2>;
+using DxTile64 = TileShape<64, 64, 1, 2, 3, 3>;
+using DxTile32 = TileShape<32, 128, 1, 4, 4, 4>;
+HeadDxPlan head_dx_plan(int64_t T, int64_t H, int64_t cols);
+
+// Workspace of the loss (byte offsets): partial maxima and sums [slots][T], the targets' logits [T].
+struct HeadLayout {
+  size_t at_target = 0, total = 0;
+  int64_t slots = 0;
+};
+HeadLayout head_layout(int64_t T, int64_t V, int64_t H);
+// Workspace of its gradient: a piece of the logits' gradient over c, [T][pitch] bf16; c and its inverse without
+// d_loss [2][T]; bf16(c x) [T][H]; the sums of dx [parts][T][H] FP32 unless one part of one piece is all there is.
+struct HeadBwdLayout {
+  int64_t cols = 0, pieces = 0, pitch = 0;   // columns of a piece; its row length
+  HeadDxPlan dx = {};
+  size_t c = 0, xc = 0, sums = 0, total = 0;
+  bool direct() const { return pieces == 1 && dx.parts == 1; }
+};
+constexpr int64_t kHeadPieceBytes = int64_t(512) << 20;
+HeadBwdLayout head_bwd_layout(int64_t T, int64_t V, int64_t H);
+bool head_grid_fits(int64_t T, int64_t V, int64_t H);
+
+// ---- AdamW step ----
+// A workgroup's chunk: kAdamwUnroll blocks of 256 values a wave. Tensors of a launch: what the kernel's
+// arguments (4 KB) hold.
+constexpr int kAdamwThreads = 256, kAdamwUnroll = 4, kAdamwChunkBlocks = kAdamwThreads / 64 * kAdamwUnroll;
+constexpr int kAdamwTensors = 54;
+constexpr int64_t kAdamwMostChunks = (int64_t(1) << 32) / kAdamwThreads - 1;   // threads of a launch
+constexpr int64_t kAdamwMostValues = kAdamwMostChunks * kAdamwChunkBlocks * 256;
+inline int64_t adamw_chunks(int64_t count) { return ceil_div(count, kAdamwChunkBlocks * 256); }
+
+bool gated_grid_fits(int64_t R, int64_t E, int64_t Fw, int64_t K);
+bool gated_bwd_grid_fits(int64_t R, int64_t E, int64_t Fw, int64_t H);
+
+}  // namespace beam

@@ -180,14 +180,16 @@ constexpr TileCost rows_cost(Tile192) { return {.235, .1, 3.2, .59, 0.}; }
 constexpr TileCost rows_cost(Tile256Deep) { return {.25, .1, 2.4, .83, 0.}; }
 constexpr TileCost rows_cost(Tile320) { return {.28, .1, 2.3, 1.0, 0.}; }
 
-template <class F>
-void with_rows_tile(int64_t R, int64_t E, int64_t No, int64_t Kc, bool out_bf16, F&& f) {
-  const double full = (double)std::min(R, E), mean = (double)R / full;
-  const double w_mb = full * No * Kc * 2e-6;
-  const double mb = w_mb + R * (Kc * 2e-6 + No * (out_bf16 ? 2e-6 : 4e-6));
-  const double stages = (double)ceil_div(Kc, 64);
-  auto us = [&](auto s) {
-    using S = decltype(s);
+// A call of R rows, E experts, contraction Kc, whose tiles cover No columns of weights and move `mb`
+// megabytes, of them w_mb of weights, with tile shape S.
+struct RowsCall {
+  double full, mean, w_mb, mb, stages;
+  int64_t E, No;
+  RowsCall(int64_t R, int64_t E_, int64_t No_, int64_t Kc, double out_mb)
+      : full((double)std::min(R, E_)), mean((double)R / full), w_mb(full * No_ * Kc * 2e-6),
+        mb(w_mb + R * Kc * 2e-6 + out_mb), stages((double)ceil_div(Kc, 64)), E(E_), No(No_) {}
+  template <class S>
+  double us(S s) const {
     const TileCost c = rows_cost(s);
     double blocks = std::ceil(mean / S::BM);   // of an expert
     if (E > 1)
@@ -195,9 +197,14 @@ void with_rows_tile(int64_t R, int64_t E, int64_t No, int64_t Kc, bool out_bf16,
     const double rounds = std::ceil(full * blocks * ceil_div(No, S::BN) / kSlots<S> - 1e-9);
     return std::max(4.3 + rounds * (c.ends + stages * c.stage),
                     mb * c.mb + w_mb * (blocks - 1.0) * c.l2_mb);
-  };
-  with_least(us, f, TileStream{}, TileLone{}, Tile64{}, TilePair{}, Tile128{}, Tile192{}, Tile256Deep{},
-             Tile320{});
+  }
+};
+
+template <class F>
+void with_rows_tile(int64_t R, int64_t E, int64_t No, int64_t Kc, bool out_bf16, F&& f) {
+  const RowsCall call(R, E, No, Kc, R * (No * (out_bf16 ? 2e-6 : 4e-6)));
+  with_least([&](auto s) { return call.us(s); }, f, TileStream{}, TileLone{}, Tile64{}, TilePair{}, Tile128{},
+             Tile192{}, Tile256Deep{}, Tile320{});
 }
 
 // Weight gradient. Measured (us) with 256 x 256, 128 x 128 and 64 x 128 tiles: 32 experts of 1024 rows,
