@@ -425,8 +425,10 @@ BEAM_API size_t beam_head_loss_backward_workspace_bytes(int64_t T, int64_t V, in
  * A state, its root and their rounding are correctly rounded FP32 operations without fused ones. 8-bit roots
  * above zero stay above zero (at least 2^-9 of the scale). A gradient that is not finite makes its value's
  * state and weight so, and with 8-bit states its block's.
- * beam_moe_adamw checks each tensor by itself; beam_moe_adamw_check, for a list made once, also that no two of
- * the list's arrays overlap (gradients may share memory).
+ * beam_moe_adamw checks each tensor by itself. A list that is used again should have a table: beam_moe_adamw_table
+ * checks it as a whole (no two arrays may overlap; gradients may share memory) and writes the table to HOST memory
+ * of at least beam_moe_adamw_table_bytes(tensors, n); the caller copies it to the device (16-byte aligned) and hands
+ * that in with the same list, and the step is one launch. device_table = NULL: a launch for every 54 tensors.
  * Limits: 0 <= beta < 1, 1e-30 <= eps <= 1e30, count under 2^36, fewer than 2^39 values in all. No workspace;
  * n = 0 is a no-op. */
 typedef struct beam_adamw_tensor {
@@ -451,9 +453,11 @@ typedef struct beam_adamw_cfg {
 } beam_adamw_cfg;
 BEAM_API beam_status_t beam_moe_adamw(const beam_adamw_tensor* tensors, int32_t n, int32_t param_dtype,
                                       int32_t grad_dtype, int32_t state_dtype, const beam_adamw_cfg* cfg,
-                                      void* stream);
-BEAM_API beam_status_t beam_moe_adamw_check(const beam_adamw_tensor* tensors, int32_t n,
-                                            int32_t param_dtype, int32_t grad_dtype, int32_t state_dtype);
+                                      const void* device_table, void* stream);
+BEAM_API size_t beam_moe_adamw_table_bytes(const beam_adamw_tensor* tensors, int32_t n);
+BEAM_API beam_status_t beam_moe_adamw_table(const beam_adamw_tensor* tensors, int32_t n,
+                                            int32_t param_dtype, int32_t grad_dtype, int32_t state_dtype,
+                                            void* table, size_t table_bytes);
 
 /* Dynamic FP8 E4M3 quantisation of bf16 rows, the activation step of the FP8 experts (dynamic FP8
  * checkpoints: [S] §Highlights, §BF16, NVFP4 and FP8 Model Support).

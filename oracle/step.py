@@ -125,9 +125,13 @@ def to_eight_bits(x, bits16=None, root=False):
     if bits16 is None:
         q = codecs.e4m3_decode(codecs.e4m3_encode(t.astype(np.float64)))
     else:
-        e = np.maximum(np.frexp(t.astype(np.float64))[1] - 1, -6)
-        up = t * (2.0 ** (3 - e)).astype(F32) + blocks(np.asarray(bits16, dtype=F32)) * F32(2.0 ** -16)
-        q = np.minimum(np.floor(up) * (2.0 ** (e - 3)).astype(F32), F32(448))
+        # up with a probability of the distance in steps: 2^-3 of the binade, 2^-9 below 2^-6, where a value
+        # is rounded to 2^-29 first
+        t = t.astype(np.float64)
+        t = np.where(t < 2.0 ** -6, np.rint(t * 2.0 ** 29) * 2.0 ** -29, t)
+        e = np.maximum(np.frexp(t)[1] - 1, -6)
+        up = t * 2.0 ** (3 - e) + blocks(np.asarray(bits16, dtype=np.float64)) * 2.0 ** -16
+        q = np.minimum(np.floor(up) * 2.0 ** (e - 3), 448.0)
     if root:
         q = np.where((b > 0) & (q < 2.0 ** -9), 2.0 ** -9, q)
     q = np.copysign(np.asarray(q, dtype=np.float64), b).reshape(-1)[: len(x)]

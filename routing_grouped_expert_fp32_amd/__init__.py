@@ -165,10 +165,12 @@ def lib() -> ctypes.CDLL:
             getattr(L, name).argtypes = [i64, i64, i32]
             getattr(L, name).restype = sz
         tensors = ctypes.POINTER(_AdamWTensor)
-        L.beam_moe_adamw.argtypes = [tensors, i32, i32, i32, i32, ctypes.POINTER(_AdamWCfg), vp]
+        L.beam_moe_adamw.argtypes = [tensors, i32, i32, i32, i32, ctypes.POINTER(_AdamWCfg), vp, vp]
         L.beam_moe_adamw.restype = i32
-        L.beam_moe_adamw_check.argtypes = [tensors, i32, i32, i32, i32]
-        L.beam_moe_adamw_check.restype = i32
+        L.beam_moe_adamw_table_bytes.argtypes = [tensors, i32]
+        L.beam_moe_adamw_table_bytes.restype = sz
+        L.beam_moe_adamw_table.argtypes = [tensors, i32, i32, i32, i32, vp, sz]
+        L.beam_moe_adamw_table.restype = i32
         L.beam_moe_convert.argtypes = [vp, i64, i32, vp, vp]
         L.beam_moe_convert.restype = i32
         _LIB = L
@@ -728,8 +730,9 @@ def head_loss_backward(x, w, targets, lse, d_loss, softcap: float = 0.0, dx=None
 
 
 class AdamWPlan:
-    """The tensors of an AdamW step (adamw_plan), which it holds, and their table for the C ABI."""
-    __slots__ = ("tensors", "table", "grads", "dtypes", "device")
+    """The tensors of an AdamW step (adamw_plan), which it holds, and their table, on the host for the C ABI
+    and on the device for the launch."""
+    __slots__ = ("tensors", "table", "grads", "dtypes", "device", "on_device")
 
 
 def _adamw_grads(plan, grads):
@@ -747,7 +750,7 @@ def adamw_plan(params, grads, m, v, m_scales=None, v_scales=None, copies=None) -
     fp32 or all bf16), grads (all fp32 or all bf16), and states m, v of the params' shapes, fp32, or
     float8_e4m3fn (uint8 codes) with m_scales, v_scales: fp32 of ceil(count / 256) values. copies: bf16
     tensors that take the updated fp32 weights. The plan keeps the tensors and their addresses: make
-    another if their storage is replaced. No two tensors may overlap (beam_moe_adamw_check)."""
+    another if their storage is replaced. No two tensors may overlap (beam_moe_adamw_table)."""
     params, grads, m, v = list(params), list(grads), list(m), list(v)
     n, f32, bf = len(params), torch.float32, torch.bfloat16
     eight = n > 0 and m[:1] != [] and m[0].dtype != f32
@@ -784,9 +787,12 @@ def adamw_plan(params, grads, m, v, m_scales=None, v_scales=None, copies=None) -
     plan.grads, plan.table = grads, table
     plan.dtypes = (_DT_CODE[pdt], _DT_CODE[gdt], BEAM_FP8_E4M3 if eight else BEAM_F32)
     plan.device = _device_of(*params, *grads, *m, *v, *scales[0], *scales[1], *copies_)
-    rc = lib().beam_moe_adamw_check(table, n, *plan.dtypes)
+    host = torch.empty(lib().beam_moe_adamw_table_bytes(table, n), dtype=torch.uint8)
+    rc = lib().beam_moe_adamw_table(table, n, *plan.dtypes, host.data_ptr(), host.numel())
     if rc != 0:
-        raise BeamError(rc, "beam_moe_adamw_check")
+        raise BeamError(rc, "beam_moe_adamw_table")
+    # from pageable memory: the copy is done when the call returns, whatever stream the steps run on
+    plan.on_device = None if plan.device is None else host.to(torch.device("cuda", plan.device))
     return plan
 
 
@@ -812,16 +818,17 @@ def adamw(plan: AdamWPlan, step, lr, betas=(0.9, 0.95), eps: float = 1e-8, weigh
     cfg = _AdamWCfg(0.0 if scalars[1] else float(lr), float(betas[0]), float(betas[1]), float(eps),
                     float(weight_decay), 0 if scalars[0] else int(step), int(seed is not None),
                     0 if seed is None else int(seed) & 0xFFFFFFFF, 0, scalars[0], scalars[1], scalars[2])
-    n, table = len(plan.grads), plan.table
+    n, table, on_device = len(plan.grads), plan.table, plan.on_device.data_ptr()
     if grads is not None:
         grads = list(grads)
         _adamw_grads(plan, grads)
         table = type(table).from_buffer_copy(table)
         for i, g in enumerate(grads):
             table[i].grad = g.data_ptr()
+        on_device = None
     ctx, st = _on(plan.device, stream)
     with ctx:
-        rc = lib().beam_moe_adamw(table, n, *plan.dtypes, ctypes.byref(cfg), st)
+        rc = lib().beam_moe_adamw(table, n, *plan.dtypes, ctypes.byref(cfg), on_device, st)
     if rc != 0:
         raise BeamError(rc, "beam_moe_adamw")
 

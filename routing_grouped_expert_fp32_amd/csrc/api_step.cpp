@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 #include <new>
 
 #include "../../include/beam_moe.h"
@@ -223,11 +224,21 @@ beam_status_t beam_head_loss_backward(const void* x, const void* w, const int32_
                   st, "head_loss_backward");
 }
 
-beam_status_t beam_moe_adamw_check(const beam_adamw_tensor* tensors, int32_t n, int32_t param_dtype,
-                                   int32_t grad_dtype, int32_t state_dtype) {
+size_t beam_moe_adamw_table_bytes(const beam_adamw_tensor* tensors, int32_t n) {
+  size_t bytes = 16;
+  for (int32_t i = 0; tensors && i < n; ++i)
+    if (tensors[i].count > 0)
+      bytes += sizeof(beam::AdamwEntry) + 4 * (size_t)beam::adamw_chunks(std::min(tensors[i].count, beam::kAdamwMostValues));
+  return bytes;
+}
+
+beam_status_t beam_moe_adamw_table(const beam_adamw_tensor* tensors, int32_t n, int32_t param_dtype, int32_t grad_dtype,
+                                   int32_t state_dtype, void* table, size_t table_bytes) {
   beam_status_t rc = check_adamw_types(n, param_dtype, grad_dtype, state_dtype);
   if (rc == BEAM_OK) rc = check_adamw_tensors(tensors, n, param_dtype, grad_dtype, state_dtype);
   if (rc != BEAM_OK || n == 0) return rc;
+  if (!table) return BEAM_ERR_NULL;
+  if (table_bytes < beam_moe_adamw_table_bytes(tensors, n)) return BEAM_ERR_WORKSPACE;
   struct Piece {
     Range r;
     bool out;
@@ -251,11 +262,30 @@ beam_status_t beam_moe_adamw_check(const beam_adamw_tensor* tensors, int32_t n, 
     end = std::max(end, all[i].r.hi);
   }
   delete[] all;
-  return rc;
+  if (rc != BEAM_OK) return rc;
+  size_t used = 0;
+  for (int32_t i = 0; i < n; ++i) used += tensors[i].count > 0;
+  char* const entries = reinterpret_cast<char*>(table);
+  char* const map = entries + used * sizeof(beam::AdamwEntry);
+  int64_t chunks = 0, base = 0;
+  int32_t k = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    if (tensors[i].count == 0) continue;
+    beam::AdamwEntry e;
+    std::memcpy(&e.t, &tensors[i], sizeof(e.t));
+    e.first = (int32_t)chunks;
+    e.base256 = (int32_t)base;
+    std::memcpy(entries + k * sizeof(e), &e, sizeof(e));
+    for (const int64_t end = chunks + beam::adamw_chunks(tensors[i].count); chunks < end; ++chunks)
+      std::memcpy(map + 4 * chunks, &k, 4);
+    base += beam::ceil_div(tensors[i].count, 256);
+    ++k;
+  }
+  return BEAM_OK;
 }
 
 beam_status_t beam_moe_adamw(const beam_adamw_tensor* tensors, int32_t n, int32_t param_dtype, int32_t grad_dtype,
-                             int32_t state_dtype, const beam_adamw_cfg* cfg, void* stream) {
+                             int32_t state_dtype, const beam_adamw_cfg* cfg, const void* device_table, void* stream) {
   beam_status_t rc = check_adamw_types(n, param_dtype, grad_dtype, state_dtype);
   if (rc != BEAM_OK) return rc;
   if (!cfg) return BEAM_ERR_NULL;
@@ -265,6 +295,7 @@ beam_status_t beam_moe_adamw(const beam_adamw_tensor* tensors, int32_t n, int32_
       !(c.eps >= 1e-30 && c.eps <= 1e30) || (!c.step_on_device && c.step < 1))
     return BEAM_ERR_SHAPE;
   if ((rc = check_adamw_tensors(tensors, n, param_dtype, grad_dtype, state_dtype)) != BEAM_OK) return rc;
+  if (!aligned16(device_table)) return BEAM_ERR_ALIGN;
   if (((uintptr_t)c.step_on_device | (uintptr_t)c.lr_on_device | (uintptr_t)c.grad_scale) % 4 != 0)
     return BEAM_ERR_ALIGN;
   bool some = false, copies = false;
@@ -296,8 +327,8 @@ beam_status_t beam_moe_adamw(const beam_adamw_tensor* tensors, int32_t n, int32_
                     offsetof(beam::AdamwTensor, count) == offsetof(beam_adamw_tensor, count),
                 "one layout");
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  return launched(beam::launch_adamw(reinterpret_cast<const beam::AdamwTensor*>(tensors), n, param_dtype == BEAM_BF16,
-                                     grad_dtype == BEAM_BF16, state_dtype == BEAM_FP8_E4M3, copies, c.stochastic != 0,
+  return launched(beam::launch_adamw(reinterpret_cast<const beam::AdamwTensor*>(tensors), n, device_table,
+                                     param_dtype == BEAM_BF16, grad_dtype == BEAM_BF16, state_dtype == BEAM_FP8_E4M3, copies, c.stochastic != 0,
                                      s, st),
                   st, "adamw");
 }

@@ -233,6 +233,7 @@ struct AdamwScalars {
   const float* lr_now;                // lr on the device (nullable)
   const float* grad_scale;            // nullable: 1
 };
-hipError_t launch_adamw(const AdamwTensor* tensors, int n, bool p_bf16, bool g_bf16, bool q8, bool copy,
-                        bool noise, const AdamwScalars& s, hipStream_t st);
+// `table`: the list's table on the device (adamw_table), or null.
+hipError_t launch_adamw(const AdamwTensor* tensors, int n, const void* table, bool p_bf16, bool g_bf16, bool q8,
+                        bool copy, bool noise, const AdamwScalars& s, hipStream_t st);
 }  // namespace beam

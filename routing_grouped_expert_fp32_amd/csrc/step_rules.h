@@ -80,10 +80,16 @@ HeadBwdLayout head_bwd_layout(int64_t T, int64_t V, int64_t H);
 bool head_grid_fits(int64_t T, int64_t V, int64_t H);
 
 // ---- AdamW step ----
-// A workgroup's chunk: kAdamwUnroll blocks of 256 values a wave. Tensors of a launch: what the kernel's
-// arguments (4 KB) hold.
+// A workgroup's chunk: kAdamwUnroll blocks of 256 values a wave. Tensors of a launch without a table: what the
+// kernel's arguments (4 KB) hold. A table: an entry for each tensor that has values, then each chunk's entry.
+struct AdamwEntry {
+  AdamwTensor t;
+  int32_t first;     // its first chunk
+  int32_t base256;   // blocks of 256 values before it in the whole list
+};
 constexpr int kAdamwThreads = 256, kAdamwUnroll = 4, kAdamwChunkBlocks = kAdamwThreads / 64 * kAdamwUnroll;
 constexpr int kAdamwTensors = 54;
+static_assert(sizeof(AdamwEntry) == 72, "one layout on host and device");
 constexpr int64_t kAdamwMostChunks = (int64_t(1) << 32) / kAdamwThreads - 1;   // threads of a launch
 constexpr int64_t kAdamwMostValues = kAdamwMostChunks * kAdamwChunkBlocks * 256;
 inline int64_t adamw_chunks(int64_t count) { return ceil_div(count, kAdamwChunkBlocks * 256); }

@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
+#include <cstring>
 #include <random>
 #include <vector>
 
@@ -139,15 +140,39 @@ void adamw_calls(int n, int32_t p, int32_t g, int32_t s, bool copy) {
   cfg.beta2 = 0.95;
   cfg.eps = 1e-8;
   cfg.step = 4;
-  expect(beam_moe_adamw_check(t.data(), n, p, g, s) == BEAM_OK, "adamw_check", n);
-  expect(beam_moe_adamw(t.data(), n, p, g, s, &cfg, nullptr) == BEAM_OK, "adamw", n);
+  std::vector<char> table(beam_moe_adamw_table_bytes(t.data(), n));
+  auto check = [&]() { return beam_moe_adamw_table(t.data(), n, p, g, s, table.data(), table.size()); };
+  expect(check() == BEAM_OK, "adamw_table", n);
+  expect(n == 0 || beam_moe_adamw_table(t.data(), n, p, g, s, table.data(), table.size() - 1) == BEAM_ERR_WORKSPACE,
+         "adamw_table bytes", n);
+  // every chunk's entry, and the blocks before it
+  int32_t used = 0;
+  for (auto& a : t) used += a.count > 0;
+  int64_t chunk = 0, blocks = 0;
+  int32_t k = 0;
+  for (auto& a : t) {
+    if (a.count == 0) continue;
+    beam::AdamwEntry e;
+    std::memcpy(&e, table.data() + k * sizeof(e), sizeof(e));
+    expect(e.t.param == a.param && e.t.count == a.count && e.first == chunk && e.base256 == blocks, "an entry", n, k);
+    for (int64_t c = 0; c < beam::adamw_chunks(a.count); ++c, ++chunk) {
+      int32_t at;
+      std::memcpy(&at, table.data() + used * sizeof(e) + 4 * chunk, 4);
+      expect(at == k, "a chunk's entry", n, k, chunk);
+    }
+    blocks += ceil_div(a.count, 256);
+    ++k;
+  }
+  void* on_device = buf(table.size(), "table");
+  expect(beam_moe_adamw(t.data(), n, p, g, s, &cfg, nullptr, nullptr) == BEAM_OK, "adamw", n);
+  expect(beam_moe_adamw(t.data(), n, p, g, s, &cfg, on_device, nullptr) == BEAM_OK, "adamw with its table", n);
   if (n > 1 && t[0].count > 300 && t[n - 1].count > 300) {   // arrays of two tensors that meet
     void* const was = t[0].m;
     t[0].m = (char*)t[n - 1].param + 16;
-    expect(beam_moe_adamw_check(t.data(), n, p, g, s) == BEAM_ERR_ALIAS, "adamw_check overlap", n);
+    expect(check() == BEAM_ERR_ALIAS, "adamw_check overlap", n);
     t[0].m = was;
     t[0].grad = t[n - 1].grad;   // gradients may
-    if (t[0].count <= t[n - 1].count) expect(beam_moe_adamw_check(t.data(), n, p, g, s) == BEAM_OK, "shared grads", n);
+    if (t[0].count <= t[n - 1].count) expect(check() == BEAM_OK, "shared grads", n);
   }
   release();
 }

@@ -94,7 +94,8 @@ def test_head_no_tokens_and_sizes():
     assert bm.head_loss_workspace_bytes(4096, 131072, 5120) < 64 << 20
 
 
-def _adamw(n=2, p=bm.BEAM_F32, g=bm.BEAM_BF16, s=bm.BEAM_F32, cfg=True, check=False, tensors=True, **kw):
+def _adamw(n=2, p=bm.BEAM_F32, g=bm.BEAM_BF16, s=bm.BEAM_F32, cfg=True, check=False, tensors=True, on_device=None, room=4096,
+           **kw):
     t = (bm._AdamWTensor * 2)()
     size = 1 << 16
     for i in range(2):
@@ -111,8 +112,9 @@ def _adamw(n=2, p=bm.BEAM_F32, g=bm.BEAM_BF16, s=bm.BEAM_F32, cfg=True, check=Fa
             setattr(t[1], k, v)
     table = t if tensors else None
     if check:
-        return bm.lib().beam_moe_adamw_check(table, n, p, g, s)
-    return bm.lib().beam_moe_adamw(table, n, p, g, s, ctypes.byref(bm._AdamWCfg(**c)) if cfg else None, None)
+        host = (ctypes.c_char * 4096)()
+        return bm.lib().beam_moe_adamw_table(table, n, p, g, s, host, room)
+    return bm.lib().beam_moe_adamw(table, n, p, g, s, ctypes.byref(bm._AdamWCfg(**c)) if cfg else None, on_device, None)
 
 
 @pytest.mark.parametrize("check", [False, True])
@@ -147,8 +149,12 @@ def test_adamw_numbers():
         assert _adamw(**{k: A[9] + 2}) == ALIGN, k
 
 
-def test_adamw_check_overlaps():
+def test_adamw_table():
     size = 1 << 16
+    need = 16 + 2 * (72 + 4)
+    assert _adamw(check=True, room=need - 1) == WORKSPACE and _adamw(check=True, room=need) == OK
+    assert _adamw(on_device=A[9] + 8) == ALIGN
+    assert bm.lib().beam_moe_adamw_table(None, 0, 0, 0, 0, None, 0) == OK
     assert _adamw(check=True) == OK
     assert _adamw(check=True, grad=A[0] + size) == OK                # both tensors' gradients in one place
     assert _adamw(check=True, param=A[0]) == ALIAS                   # the first tensor's weights
@@ -164,7 +170,7 @@ def test_valid_calls_without_gpu_report_device():
     assert _head() == DEVICE and _head(cap=30.0) == DEVICE
     assert _hbwd() == DEVICE and _hbwd(dt=bm.BEAM_F32, cap=30.0) == DEVICE
     assert _hbwd(T=0, x=None, w=None, y=None, lse=None, d=None, dx=None, ws=None, nb=0) == DEVICE
-    assert _adamw() == DEVICE and _adamw(s=bm.BEAM_FP8_E4M3) == DEVICE and _adamw(step=0, step_on_device=A[9]) == DEVICE
+    assert _adamw() == DEVICE and _adamw(on_device=A[9]) == DEVICE and _adamw(s=bm.BEAM_FP8_E4M3) == DEVICE and _adamw(step=0, step_on_device=A[9]) == DEVICE
 
 
 def test_binding_refuses_mismatched_tensors():
