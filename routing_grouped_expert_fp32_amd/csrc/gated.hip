@@ -21,6 +21,13 @@
 
 namespace beam {
 
+// 1 / (1 + e^-g) with the hardware's exponential and reciprocal: off by (2 + |g|) 2^-23 of it, which the bf16
+// results do not show; its limits where e^-g is 0 or infinite. (Full-precision ones, some 40 instructions a
+// value, made the gradient of 32768 skewed rows 3% slower.)
+__device__ __forceinline__ float sigmoid_fast(float g) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g * -1.442695041f));
+}
+
 // One tile: rows of `blk`, hidden values from col0 on.
 template <class S, bool KEEP>
 __device__ __forceinline__ void gated_tile(const unsigned char* __restrict__ x,
@@ -67,9 +74,10 @@ __device__ __forceinline__ void gated_tile(const unsigned char* __restrict__ x,
         const u32x2 ub = {pack_bf16(u.x, u.y), pack_bf16(u.z, u.w)};
         const floatx4 gv = rounded ? floatx4{bf16_lo(gb.x), bf16_hi(gb.x), bf16_lo(gb.y), bf16_hi(gb.y)} : g;
         const floatx4 uv = rounded ? floatx4{bf16_lo(ub.x), bf16_hi(ub.x), bf16_lo(ub.y), bf16_hi(ub.y)} : u;
-        const float h0 = silu_f32(gv.x) * uv.x, h1 = silu_f32(gv.y) * uv.y;
-        const float h2 = silu_f32(gv.z) * uv.z, h3 = silu_f32(gv.w) * uv.w;
-        *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16(h0, h1), pack_bf16(h2, h3)};
+        floatx4 hv;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) hv[c] = gv[c] * sigmoid_fast(gv[c]) * uv[c];
+        *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16(hv.x, hv.y), pack_bf16(hv.z, hv.w)};
         if constexpr (KEEP) {
           *reinterpret_cast<u32x2*>(p + kPart) = gb;
           *reinterpret_cast<u32x2*>(p + 2 * kPart) = ub;
@@ -197,7 +205,7 @@ __device__ __forceinline__ void gated_bwd_tile(const GatedBwdArgs& a, const RowB
         for (int c = 0; c < 8; ++c) {
           const float g = c & 1 ? bf16_hi(t.g[c / 2]) : bf16_lo(t.g[c / 2]);
           const float u = c & 1 ? bf16_hi(t.u[c / 2]) : bf16_lo(t.u[c / 2]);
-          const float sig = 1.f / (1.f + expf(-g)), act = g * sig, hc = act * u;
+          const float sig = sigmoid_fast(g), act = g * sig, hc = act * u;
           if constexpr (SCALED) sum += dh[c] * hc;
           const float d = SCALED ? t.s * dh[c] : dh[c];
           dg[c] = d * u * (sig * (1.f + g * (1.f - sig)));

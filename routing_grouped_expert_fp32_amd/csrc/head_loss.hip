@@ -175,28 +175,33 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   }
 }
 
-// lse and loss of 16 rows a workgroup: 64 threads a row join every 64th slot, then the 64 in order.
-constexpr int kJoinRows = 16, kJoinThreads = 64;
-__global__ __launch_bounds__(kJoinRows * kJoinThreads) void head_join_kernel(
+// lse and loss of kJoinRows rows a workgroup: kJoinWays threads a row join every kJoinWays-th slot, then their
+// results pair by pair. Few tokens: four rows and 128 threads each (32 tokens, 1024 slots: 4.2 us, 16 rows of 64
+// 11); more: 16 rows of 32, a line of 128 bytes a slot (4096 tokens, 1024 slots: 9 us, four rows 25).
+template <int kJoinRows, int kJoinWays>
+__global__ __launch_bounds__(kJoinRows * kJoinWays) void head_join_kernel(
     const float2* __restrict__ stats, const float* __restrict__ at_target, const int32_t* __restrict__ targets,
     float* __restrict__ loss, float* __restrict__ lse_out, int slots, int T, int vocab) {
-  __shared__ float2 part[kJoinThreads][kJoinRows];
+  __shared__ float2 part[kJoinWays][kJoinRows];
   const int r = threadIdx.x % kJoinRows, k = threadIdx.x / kJoinRows;
   const int t = blockIdx.x * kJoinRows + r;
   float top = -INFINITY, sum = 0.f;
   auto join = [&](float2 o) {
     const float m = fmaxf(top, o.x), from = m == -INFINITY ? 0.f : m;
-    sum = sum * expf(top - from) + o.y * expf(o.x - from);
+    sum = sum * exp_fast(top - from) + o.y * exp_fast(o.x - from);
     top = m;
   };
   if (t < T) {
-#pragma unroll 4
-    for (int s = k; s < slots; s += kJoinThreads) join(stats[(int64_t)s * T + t]);
+#pragma unroll 8
+    for (int s = k; s < slots; s += kJoinWays) join(stats[(int64_t)s * T + t]);
   }
-  part[k][r] = make_float2(top, sum);
-  __syncthreads();
+#pragma unroll
+  for (int n = kJoinWays / 2; n > 0; n >>= 1) {
+    if (k >= n && k < 2 * n) part[k][r] = make_float2(top, sum);
+    __syncthreads();
+    if (k < n) join(part[k + n][r]);
+  }
   if (k > 0 || t >= T) return;
-  for (int o = 1; o < kJoinThreads; ++o) join(part[o][r]);
   const float lse = top + logf(sum);
   const int y = targets[t];
   lse_out[t] = lse;
@@ -423,8 +428,15 @@ hipError_t launch_head_loss(const HeadArgs& h, float* loss, float* lse, char* ws
   launch_logits<false>(a, a.V, st);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(head_join_kernel, dim3((unsigned)ceil_div(h.T, kJoinRows)), dim3(kJoinRows * kJoinThreads), 0, st,
-                     a.stats, a.at_target, a.targets, loss, lse, (int)L.slots, a.T, a.vocab);
+  auto join = [&](auto rows, auto ways) {
+    constexpr int kRows = decltype(rows)::value, kWays = decltype(ways)::value;
+    hipLaunchKernelGGL((head_join_kernel<kRows, kWays>), dim3((unsigned)ceil_div(h.T, kRows)), dim3(kRows * kWays), 0, st,
+                       a.stats, a.at_target, a.targets, loss, lse, (int)L.slots, a.T, a.vocab);
+  };
+  if (h.T < 1024)
+    join(std::integral_constant<int, 4>{}, std::integral_constant<int, 128>{});
+  else
+    join(std::integral_constant<int, 16>{}, std::integral_constant<int, 32>{});
   return hipGetLastError();
 }
 
