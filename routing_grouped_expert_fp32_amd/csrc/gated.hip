@@ -113,7 +113,7 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   RowBlock blk;
   int ctile, half;
-  if (!row_block_tile<S>(offsets, R, E, n_ctiles, max_blocks, lane, blk, ctile, half)) return;
+  if (!row_block_tile<S, true>(offsets, R, E, n_ctiles, max_blocks, lane, blk, ctile, half)) return;
   const int col0 = ctile * kGatedCols<S>;
   if constexpr (kHalves<S>) {
     if (half >= 0) {
@@ -246,7 +246,7 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   RowBlock blk;
   int ctile, half;
-  if (!row_block_tile<S>(a.offsets, a.R, a.E, n_ctiles, max_blocks, lane, blk, ctile, half)) return;
+  if (!row_block_tile<S, true>(a.offsets, a.R, a.E, n_ctiles, max_blocks, lane, blk, ctile, half)) return;
   const int col0 = ctile * S::BN;
   if constexpr (kHalves<S>) {
     if (half >= 0) {

@@ -86,8 +86,8 @@ struct BlockScan {
 };
 
 // Tile of a workgroup: the block's rows, its column tile and, for the last tiles of a launch, which
-// column half (else -1). False: none.
-template <class S>
+// column half (else -1). False: none. DEALT: tiles dealt to the XCDs by xcd_tile_dealt.
+template <class S, bool DEALT = false>
 __device__ __forceinline__ bool row_block_tile(const int32_t* __restrict__ offsets, int R, int E,
                                                int n_ctiles, int max_blocks, int lane, RowBlock& blk,
                                                int& ctile, int& half) {
@@ -95,7 +95,7 @@ __device__ __forceinline__ bool row_block_tile(const int32_t* __restrict__ offse
   scan.init(offsets, E, R, lane);
   // more blocks than the grid has come only from offsets that are not in order
   const int total = min(scan.total, max_blocks) * n_ctiles;
-  const int v = xcd_tile_halves<S>(blockIdx.x, total, half);
+  const int v = DEALT ? xcd_tile_dealt<S>(blockIdx.x, total, half) : xcd_tile_halves<S>(blockIdx.x, total, half);
   if (v < 0) return false;
   blk = scan.find(v / n_ctiles);
   if (blk.rows <= 0) return false;

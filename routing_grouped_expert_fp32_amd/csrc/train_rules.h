@@ -63,6 +63,19 @@ constexpr int xcd_tile_halves(int wg, int total, int& half) {
   }
   return local < mine ? first + local : -1;
 }
+// The same where tiles are of unequal height in runs (an expert's blocks are alike, another's are not):
+// an XCD takes every eighth run of 32 tiles instead of one eighth of them all, so that none has the tall ones
+// alone; the tiles behind the last 256 are cut into eight runs as above.
+template <class S>
+constexpr int xcd_tile_dealt(int wg, int total, int& half) {
+  const int rounds = total / (8 * kXcdCus), whole = rounds * kXcdCus;
+  const int xcd = wg & 7, local = wg >> 3;
+  half = -1;
+  if (local < whole) return (local / kXcdCus * 8 + xcd) * kXcdCus + local % kXcdCus;
+  // the rest of an XCD's tiles begins where its CUs get free: fewer than 32, as a tail above
+  const int t = xcd_tile_halves<S>((local - whole) << 3 | xcd, total - 8 * whole, half);
+  return t < 0 ? -1 : 8 * whole + t;
+}
 template <class S>
 int64_t xcd_workgroups_halves(int64_t tiles) {
   return 8 * (ceil_div(tiles, 8) + (kHalves<S> ? kXcdCus / 2 : 0));

@@ -177,6 +177,27 @@ void adamw_calls(int n, int32_t p, int32_t g, int32_t s, bool copy) {
   release();
 }
 
+// Every tile of a deal to one workgroup, whole or as its two halves.
+template <class S>
+void dealt(int total) {
+  std::vector<int> whole(total, 0), halves(2 * total, 0);
+  const int64_t wgs = beam::xcd_workgroups_halves<S>(total + pick(0, 40));   // a bound: the host knows no more
+  for (int64_t wg = 0; wg < wgs; ++wg) {
+    int half = 0;
+    const int t = beam::xcd_tile_dealt<S>((int)wg, total, half);
+    if (t < 0) continue;
+    expect(t < total && half < 2 && (beam::kHalves<S> || half < 0), "a tile of the deal", total, wg, t, half);
+    if (t >= total) continue;
+    if (half < 0)
+      ++whole[t];
+    else
+      ++halves[2 * t + half];
+  }
+  for (int t = 0; t < total; ++t)
+    expect(whole[t] == 1 ? !halves[2 * t] && !halves[2 * t + 1] : !whole[t] && halves[2 * t] == 1 && halves[2 * t + 1] == 1,
+           "dealt once", total, t, whole[t], halves[2 * t]);
+}
+
 // Launches of every accepted size stay under 2^32 threads.
 void limits() {
   long fit = 0;
@@ -231,6 +252,10 @@ int main() {
   for (int i = 0; i < 60; ++i)
     adamw_calls((int)spread(1, 200), i & 1 ? BEAM_F32 : BEAM_BF16, i & 2 ? BEAM_F32 : BEAM_BF16,
                 i & 4 ? BEAM_F32 : BEAM_FP8_E4M3, (i & 1) && (i & 8));
+  for (int total = 1; total < 1600; ++total) {
+    dealt<beam::Tile320>(total);
+    if (total % 7 == 0) dealt<beam::TilePair>(total);
+  }
   limits();
   std::printf("hostcheck: %ld checks, %d failed, %ld launches checked\n", g_checks, g_fail, hostcheck::step_launches());
   return g_fail ? 1 : 0;
