@@ -646,7 +646,7 @@ def gated_mm_backward(dy, w_down, gu, offsets, row_scale=None, d_gu=None, h=None
             d_row_scale = torch.empty_like(row_scale) if d_row_scale is None else d_row_scale
             if workspace is None:
                 need = gated_mm_backward_workspace_bytes(R, F)
-                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dy.device)
+                workspace = dy.new_empty(max(need, 16), dtype=torch.uint8)
             ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         offsets = _aligned_offsets(offsets)
         rc = lib().beam_moe_gated_mm_backward(
@@ -681,7 +681,7 @@ def head_loss(x, w, targets, softcap: float = 0.0, loss=None, lse=None, workspac
         lse = x.new_empty((T,), dtype=f32) if lse is None else lse
         if workspace is None:
             need = head_loss_workspace_bytes(T, V, H)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+            workspace = x.new_empty(max(need, 16), dtype=torch.uint8)
         rc = lib().beam_head_loss(x.data_ptr(), w.data_ptr(), targets.data_ptr(), loss.data_ptr(),
                                   lse.data_ptr(), T, V, H, float(softcap), workspace.data_ptr(),
                                   workspace.numel() * workspace.element_size(), st)
@@ -719,7 +719,7 @@ def head_loss_backward(x, w, targets, lse, d_loss, softcap: float = 0.0, dx=None
         dw = w.new_empty((V, H), dtype=wdt) if dw is None else dw
         if workspace is None:
             need = head_loss_backward_workspace_bytes(T, V, H)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+            workspace = x.new_empty(max(need, 16), dtype=torch.uint8)
         rc = lib().beam_head_loss_backward(
             x.data_ptr(), w.data_ptr(), targets.data_ptr(), lse.data_ptr(), d_loss.data_ptr(),
             dx.data_ptr(), dw.data_ptr(), dw_dtype, T, V, H, float(softcap), workspace.data_ptr(),

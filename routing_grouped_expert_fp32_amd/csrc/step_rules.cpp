@@ -4,6 +4,8 @@
 namespace beam {
 
 bool gated_grid_fits(int64_t R, int64_t E, int64_t Fw, int64_t K) {
+  // the narrowest tiles' launch fits: so does any
+  if (threads_fit<Tile256>(grouped_max_blocks(R, E, 32) * ceil_div(Fw, 32))) return true;
   bool ok = true;
   for (bool keep : {false, true})
     with_gated_tile(R, E, Fw, K, keep, [&](auto s) {
@@ -14,6 +16,7 @@ bool gated_grid_fits(int64_t R, int64_t E, int64_t Fw, int64_t K) {
 }
 
 bool gated_bwd_grid_fits(int64_t R, int64_t E, int64_t Fw, int64_t H) {
+  if (threads_fit<Tile256>(grouped_max_blocks(R, E, 32) * ceil_div(Fw, 64))) return true;
   bool ok = true;
   with_gated_bwd_tile(R, E, Fw, H, [&](auto s) {
     using S = decltype(s);
@@ -36,10 +39,10 @@ HeadDxPlan head_dx_plan(int64_t T, int64_t H, int64_t cols) {
   double best_us = 1e300;
   for (const Side& s : kSides) {
     const int64_t tiles = ceil_div(T, s.bm) * ceil_div(H, s.bn), slots = kGroupedCus * s.per_cu;
-    const int64_t most = std::min<int64_t>(std::max<int64_t>(1, 4 * slots / tiles), ceil_div(stages, 4));
-    for (int64_t p = 1; p <= most; ++p) {
-      const int64_t each = ceil_div(stages, p);
-      if (ceil_div(stages, each) != p) continue;
+    // one part, or what fills one to six rounds, of at least four stages each
+    for (int rounds = 0; rounds <= 6; ++rounds) {
+      const int64_t asked = std::min(std::max<int64_t>(1, rounds * slots / tiles), ceil_div(stages, 4));
+      const int64_t each = ceil_div(stages, asked), p = ceil_div(stages, each);
       double us = (double)ceil_div(tiles * p, slots) * (s.ends + (double)each * s.stage);
       // weights read once, and once more for every further row of tiles
       us = std::max(us, (double)cols * H * 2e-6 * (0.2 + 0.1 * (double)(ceil_div(T, s.bm) - 1)));
@@ -78,15 +81,18 @@ HeadBwdLayout head_bwd_layout(int64_t T, int64_t V, int64_t H) {
 }
 
 bool head_grid_fits(int64_t T, int64_t V, int64_t H) {
+  // 64 x 128 tiles of 256 threads are the weight gradient's smallest; six rounds of parts are added to x's
+  if (!threads_fit<Tile256>((ceil_div(V, 64) + 7) * (ceil_div(H, 128) + 7)) ||
+      ceil_div(T, 32) * ceil_div(H, 64) >= (int64_t(1) << 22))
+    return false;
+  if (threads_fit<Tile256>(ceil_div(T, 32) * ceil_div(V, 64))) return true;   // the narrowest tiles' launch
   bool ok = true;
   for (bool store : {false, true})
     with_head_tile(T, V, H, store, [&](auto s) {
       using S = decltype(s);
       ok = ok && threads_fit<S>(ceil_div(T, S::BM) * ceil_div(V, S::BN));
     });
-  // 64 x 128 tiles of 256 threads are the weight gradient's smallest, 64 parts of 32 x 64 tiles bound x's
-  ok = ok && threads_fit<Tile256>((ceil_div(V, 64) + 7) * (ceil_div(H, 128) + 7));
-  return ok && ceil_div(T, 32) * ceil_div(H, 64) < (int64_t(1) << 22);
+  return ok;
 }
 
 }  // namespace beam
