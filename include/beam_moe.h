@@ -355,7 +355,7 @@ BEAM_API size_t beam_moe_orthogonalise_workspace_bytes(int64_t n_mats, int32_t r
  *   dy         [R][H] bf16: gradient of the down projection's output, unscaled (of row_scale[r] y[r])
  *   w_down     [E][H][F] bf16
  *   row_scale  [R] fp32, or NULL: s = 1, d_row_scale NULL too and no workspace
- *   d_gu       [R][2 F], h [R][F] bf16 out, d_row_scale [R] fp32 out
+ *   d_gu       [R][2 F], h [R][F] bf16 out, d_row_scale [R] fp32 out (it and row_scale 4-byte aligned)
  *   workspace  with row_scale: at least beam_moe_gated_mm_backward_workspace_bytes(R, F)
  * Rows of no expert are not read, and their outputs are left as they were. R = 0 is a no-op. g of a size where
  * e^-g overflows gives the limits (sig 0 or 1). Equal calls give equal bits.
@@ -377,6 +377,7 @@ BEAM_API size_t beam_moe_gated_mm_backward_workspace_bytes(int64_t R, int32_t F)
  *   lse[t] = log sum_v e^z,  loss[t] = lse[t] - z[t][targets[t]]      (-loss: the token's log-probability)
  *   dz = d_loss[t] (e^(z - lse[t]) - [v = targets[t]]) (1 - (z / c)^2),  dx = dz w,  dw = dz^T x
  *   x          [T][H] bf16;  w [V][H] bf16
+ *   targets, loss, lse, d_loss: 4-byte aligned (views of longer arrays)
  *   targets    [T] int32; one outside [0, V) has no loss and no gradient (its loss is 0, lse is still given)
  *   loss, lse  [T] fp32 out (lse is what the gradient takes)
  *   d_loss     [T] fp32: the gradient of each token's loss (1 / T for a mean)
@@ -388,7 +389,7 @@ BEAM_API size_t beam_moe_gated_mm_backward_workspace_bytes(int64_t R, int32_t F)
  * too. The gradient works on pieces of the vocabulary, at most 512 MiB (or 512 columns) of dz at a time; the
  * loss keeps 8 bytes for each token and 64 to 256 columns. T = 0: no-ops, but dw is set to zero (the other
  * pointers may then be NULL). Equal calls give equal bits.
- * Limits: H % 8 == 0, H <= 2^20, V <= 2^23, T < 2^31, and launches of fewer than 2^32 threads. */
+ * Limits: H % 8 == 0, H <= 2^20, V <= 2^23, T < 2^24, and launches of fewer than 2^32 threads. */
 BEAM_API beam_status_t beam_head_loss(const void* x, const void* w, const int32_t* targets, float* loss,
                                       float* lse, int64_t T, int64_t V, int32_t H, float softcap,
                                       void* workspace, size_t workspace_bytes, void* stream);

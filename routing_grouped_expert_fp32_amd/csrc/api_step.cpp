@@ -37,6 +37,13 @@ bool all_aligned(const void* const (&p)[N]) {
   return std::all_of(p, p + N, aligned16);
 }
 
+// Arrays of one number a row are read and written one by one: any address of theirs will do.
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+template <size_t N>
+bool all_aligned4(const void* const (&p)[N]) {
+  return std::all_of(p, p + N, aligned4);
+}
+
 // True where an output meets an input or another output (fixed lists: no allocation, nothing thrown).
 template <size_t I, size_t O>
 bool meets(const Range (&ins)[I], const Range (&outs)[O]) {
@@ -99,7 +106,7 @@ beam_status_t check_adamw_tensors(const beam_adamw_tensor* tensors, int32_t n, i
     if (!t.param || !t.grad || !t.m || !t.v || (state == BEAM_FP8_E4M3 && (!t.m_scale || !t.v_scale)))
       return BEAM_ERR_NULL;
     const void* const wide[] = {t.param, t.grad, t.m, t.v, t.copy};
-    if (!all_aligned(wide) || ((uintptr_t)t.m_scale | (uintptr_t)t.v_scale) % 4 != 0) return BEAM_ERR_ALIGN;
+    if (!all_aligned(wide) || !aligned4(t.m_scale) || !aligned4(t.v_scale)) return BEAM_ERR_ALIGN;
     (t.copy ? copies : without) = true;
     const AdamwRanges r = adamw_ranges(t, p, g, state);
     const Range ins[] = {r.grad};
@@ -148,8 +155,8 @@ beam_status_t beam_moe_gated_mm_backward(const void* dy, const void* w_down, con
   if (!beam::gated_bwd_grid_fits(R, E, F, H)) return BEAM_ERR_UNSUPPORTED;
   const void* const ptrs[] = {dy, w_down, gu, offsets, d_gu, h};
   if (any_null(ptrs) || !row_scale != !d_row_scale || (row_scale && !workspace)) return BEAM_ERR_NULL;
-  if (!all_aligned(ptrs) || !aligned16(row_scale) || !aligned16(d_row_scale) || !aligned16(workspace))
-    return BEAM_ERR_ALIGN;
+  const void* const rows[] = {row_scale, d_row_scale};
+  if (!all_aligned(ptrs) || !all_aligned4(rows) || !aligned16(workspace)) return BEAM_ERR_ALIGN;
   const size_t need = row_scale ? beam_moe_gated_mm_backward_workspace_bytes(R, F) : 0;
   if (workspace_bytes < need) return BEAM_ERR_WORKSPACE;
   const size_t r = (size_t)R, f = (size_t)F, n = (size_t)H, e = (size_t)E, s = row_scale ? 4 * r : 0;
@@ -175,9 +182,10 @@ beam_status_t beam_head_loss(const void* x, const void* w, const int32_t* target
   beam_status_t rc = check_head(T, V, H, softcap);
   if (rc != BEAM_OK) return rc;
   if (T == 0) return BEAM_OK;
-  const void* const ptrs[] = {x, w, targets, loss, lse, workspace};
-  if (any_null(ptrs)) return BEAM_ERR_NULL;
-  if (!all_aligned(ptrs)) return BEAM_ERR_ALIGN;
+  const void* const ptrs[] = {x, w, workspace};
+  const void* const rows[] = {targets, loss, lse};
+  if (any_null(ptrs) || any_null(rows)) return BEAM_ERR_NULL;
+  if (!all_aligned(ptrs) || !all_aligned4(rows)) return BEAM_ERR_ALIGN;
   const size_t need = beam::head_layout(T, V, H).total, t = (size_t)T, v = (size_t)V, n = (size_t)H;
   if (workspace_bytes < need) return BEAM_ERR_WORKSPACE;
   const Range ins[] = {rng(x, 2 * t * n), rng(w, 2 * v * n), rng(targets, 4 * t)};
@@ -205,9 +213,10 @@ beam_status_t beam_head_loss_backward(const void* x, const void* w, const int32_
   if (!dw) return BEAM_ERR_NULL;
   if (!aligned16(dw)) return BEAM_ERR_ALIGN;
   // without tokens dw is still written (zeros), and nothing else is touched
-  const void* const ptrs[] = {x, w, targets, lse, d_loss, dx, workspace};
-  if (T > 0 && any_null(ptrs)) return BEAM_ERR_NULL;
-  if (T > 0 && !all_aligned(ptrs)) return BEAM_ERR_ALIGN;
+  const void* const ptrs[] = {x, w, dx, workspace};
+  const void* const rows[] = {targets, lse, d_loss};
+  if (T > 0 && (any_null(ptrs) || any_null(rows))) return BEAM_ERR_NULL;
+  if (T > 0 && (!all_aligned(ptrs) || !all_aligned4(rows))) return BEAM_ERR_ALIGN;
   const size_t need = T > 0 ? beam::head_bwd_layout(T, V, H).total : 0;
   if (workspace_bytes < need) return BEAM_ERR_WORKSPACE;
   const size_t t = (size_t)T, v = (size_t)V, n = (size_t)H;
@@ -296,8 +305,7 @@ beam_status_t beam_moe_adamw(const beam_adamw_tensor* tensors, int32_t n, int32_
     return BEAM_ERR_SHAPE;
   if ((rc = check_adamw_tensors(tensors, n, param_dtype, grad_dtype, state_dtype)) != BEAM_OK) return rc;
   if (!aligned16(device_table)) return BEAM_ERR_ALIGN;
-  if (((uintptr_t)c.step_on_device | (uintptr_t)c.lr_on_device | (uintptr_t)c.grad_scale) % 4 != 0)
-    return BEAM_ERR_ALIGN;
+  if (!aligned4(c.step_on_device) || !aligned4(c.lr_on_device) || !aligned4(c.grad_scale)) return BEAM_ERR_ALIGN;
   bool some = false, copies = false;
   for (int32_t i = 0; i < n; ++i) {
     some = some || tensors[i].count > 0;

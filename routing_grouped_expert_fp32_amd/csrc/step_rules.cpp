@@ -82,7 +82,8 @@ HeadBwdLayout head_bwd_layout(int64_t T, int64_t V, int64_t H) {
 
 bool head_grid_fits(int64_t T, int64_t V, int64_t H) {
   // 64 x 128 tiles of 256 threads are the weight gradient's smallest; six rounds of parts are added to x's
-  if (!threads_fit<Tile256>((ceil_div(V, 64) + 7) * (ceil_div(H, 128) + 7)) ||
+  // (and one workgroup of 256 threads a token takes its scale)
+  if (T >= (int64_t(1) << 24) || !threads_fit<Tile256>((ceil_div(V, 64) + 7) * (ceil_div(H, 128) + 7)) ||
       ceil_div(T, 32) * ceil_div(H, 64) >= (int64_t(1) << 22))
     return false;
   if (threads_fit<Tile256>(ceil_div(T, 32) * ceil_div(V, 64))) return true;   // the narrowest tiles' launch

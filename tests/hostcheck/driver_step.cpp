@@ -217,6 +217,7 @@ void limits() {
     const int64_t T = spread(1, (int64_t(1) << 31) - 1), V = spread(1, 1 << 23), H = 8 * spread(1, 1 << 17);
     if (!beam::head_grid_fits(T, V, H)) continue;
     ++fit;
+    expect(T * 256 < (int64_t(1) << 32) && ceil_div(T * H, 8 * 256) * 256 < (int64_t(1) << 32), "threads of rows", T, V, H);
     const beam::HeadBwdLayout L = beam::head_bwd_layout(T, V, H);
     const int64_t bm = L.dx.side, bn = L.dx.side == 32 ? 128 : L.dx.side;
     expect((ceil_div(T, bm) * ceil_div(H, bn) * L.dx.parts + 8) * 512 < (int64_t(1) << 32), "threads of dx", T, V, H);

@@ -224,6 +224,29 @@ def test_all_targets_dropped_and_nan_weights_of_them():
     assert not dx.any() and not dw.any()
 
 
+def test_views_of_longer_arrays():
+    """Targets one further in a longer array, rows of x and w in the middle of theirs."""
+    T, V, H = 37, 130, 40
+    x, w, y, d = [t.cuda() for t in _inputs(T, V, H)]
+    want = bm.head_loss(x, w, y)
+    grads = bm.head_loss_backward(x, w, y, want[1], d)
+
+    def inside(t, before):
+        room = torch.full((t.shape[0] + 9, *t.shape[1:]), 77, dtype=t.dtype, device="cuda")
+        room[before:before + t.shape[0]] = t
+        return room, room[before:before + t.shape[0]]
+    rooms, views = zip(*[inside(t, 1 + k) for k, t in enumerate((x, w, y, want[1], d))])
+    loss_room, loss = inside(torch.zeros_like(want[0]), 3)
+    lse_room, lse = inside(torch.zeros_like(want[0]), 1)
+    bm.head_loss(*views[:3], loss=loss, lse=lse)
+    again = bm.head_loss_backward(*views)
+    torch.cuda.synchronize()
+    assert torch.equal(loss, want[0]) and torch.equal(lse, want[1])
+    assert torch.equal(again[0], grads[0]) and torch.equal(again[1], grads[1])
+    for room, n in ((loss_room, 3), (lse_room, 1)):
+        assert (room[:n] == 77).all() and (room[n + T:] == 77).all()
+
+
 def test_repeats_streams_workspaces_and_graph():
     x, w, y, d = [t.cuda() for t in _inputs(150, 2003, 136)]
     loss, lse = bm.head_loss(x, w, y, softcap=30.0)

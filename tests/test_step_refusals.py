@@ -43,8 +43,9 @@ def test_gated_backward_refusals():
     for k in ("dy", "w", "gu", "off", "d_gu", "h"):
         assert _gbwd(**{k: None}) == NULL, k
     assert _gbwd(s=None) == NULL and _gbwd(ds=None) == NULL and _gbwd(ws=None) == NULL   # both or none
-    for k in ("dy", "w", "gu", "off", "s", "d_gu", "h", "ds", "ws"):
+    for k in ("dy", "w", "gu", "off", "d_gu", "h", "ws"):
         assert _gbwd(**{k: A[9] + 4}) == ALIGN, k
+    assert _gbwd(s=A[9] + 2) == ALIGN and _gbwd(ds=A[9] + 1) == ALIGN   # one number a row: any address of theirs
     need = bm.gated_mm_backward_workspace_bytes(100, 64)
     assert need > 0 and _gbwd(nb=need - 1) == WORKSPACE
     for o in ("d_gu", "h", "ds", "ws"):
@@ -72,11 +73,12 @@ def test_head_refusals(call):
     assert call(cap=0.01) == UNSUPPORTED and call(cap=2000.0) == UNSUPPORTED
     assert call(H=60) == UNSUPPORTED and call(H=(1 << 20) + 8) == UNSUPPORTED
     assert call(V=(1 << 23) + 1) == UNSUPPORTED and call(T=1 << 31) == UNSUPPORTED
+    assert call(T=1 << 24, H=8, V=8) == UNSUPPORTED   # a workgroup a token
     assert call(T=(1 << 31) - 1, V=1 << 23) == UNSUPPORTED   # more workgroups than 32 bits count
     names = ["x", "w", "y", "lse", "ws"] + (["loss"] if call is _head else ["d", "dx", "dw"])
     for k in names:
         assert call(**{k: None}) == NULL, k
-        assert call(**{k: A[9] + 4}) == ALIGN, k
+        assert call(**{k: A[9] + (8 if k in ("x", "w", "ws", "dx", "dw") else 2)}) == ALIGN, k
     need = (bm.head_loss_workspace_bytes if call is _head else bm.head_loss_backward_workspace_bytes)(100, 500, 64)
     assert need > 0 and call(nb=need - 1) == WORKSPACE
     ins, outs = (("x", "w", "y"), ("loss", "lse", "ws")) if call is _head else (("x", "w", "y", "lse", "d"), ("dx", "dw", "ws"))
@@ -167,7 +169,8 @@ def test_adamw_table():
 def test_valid_calls_without_gpu_report_device():
     assert _gated() == DEVICE and _gated(gu=None) == DEVICE and _gated(rounded=1) == DEVICE
     assert _gbwd() == DEVICE and _gbwd(s=None, ds=None, ws=None, nb=0) == DEVICE
-    assert _head() == DEVICE and _head(cap=30.0) == DEVICE
+    assert _head() == DEVICE and _head(cap=30.0) == DEVICE and _head(y=A[2] + 4, lse=A[4] + 12) == DEVICE
+    assert _gbwd(s=A[9] + 4, ds=A[10] + 8) == DEVICE
     assert _hbwd() == DEVICE and _hbwd(dt=bm.BEAM_F32, cap=30.0) == DEVICE
     assert _hbwd(T=0, x=None, w=None, y=None, lse=None, d=None, dx=None, ws=None, nb=0) == DEVICE
     assert _adamw() == DEVICE and _adamw(on_device=A[9]) == DEVICE and _adamw(s=bm.BEAM_FP8_E4M3) == DEVICE and _adamw(step=0, step_on_device=A[9]) == DEVICE
