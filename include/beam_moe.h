@@ -386,7 +386,7 @@ BEAM_API size_t beam_moe_gated_mm_backward_workspace_bytes(int64_t R, int32_t F)
  *   workspace  at least beam_head_loss_workspace_bytes, beam_head_loss_backward_workspace_bytes(T, V, H)
  * Logits are FP32 sums of exact products; e^z, their sums and dz are FP32. dz is rounded to bf16 for the two
  * products, whose sums are FP32 again: dx and dw carry that rounding (2^-9 of each of their terms), an FP32 dw
- * too. The gradient works on pieces of the vocabulary, at most 512 MiB (or 512 columns) of dz at a time; the
+ * too. The gradient works on pieces of the vocabulary: 512 MiB of dz at a time, or 32768 columns up to 4 GiB; the
  * loss keeps 8 bytes for each token and 64 to 256 columns. T = 0: no-ops, but dw is set to zero (the other
  * pointers may then be NULL). Equal calls give equal bits.
  * Limits: H % 8 == 0, H <= 2^20, V <= 2^23, T < 2^24, and launches of fewer than 2^32 threads. */
@@ -429,7 +429,9 @@ BEAM_API size_t beam_head_loss_backward_workspace_bytes(int64_t T, int64_t V, in
  * beam_moe_adamw checks each tensor by itself. A list that is used again should have a table: beam_moe_adamw_table
  * checks it as a whole (no two arrays may overlap; gradients may share memory) and writes the table to HOST memory
  * of at least beam_moe_adamw_table_bytes(tensors, n); the caller copies it to the device (16-byte aligned) and hands
- * that in with the same list, and the step is one launch. device_table = NULL: a launch for every 54 tensors.
+ * that in with the same list, and the step is one launch. (The table's tensors are what is updated; one of another
+ * number of tensors or fewer chunks than the list's does no more than it holds.) device_table = NULL: a launch for
+ * every 54 tensors.
  * Limits: 0 <= beta < 1, 1e-30 <= eps <= 1e30, count under 2^36, fewer than 2^39 values in all. No workspace;
  * n = 0 is a no-op. */
 typedef struct beam_adamw_tensor {

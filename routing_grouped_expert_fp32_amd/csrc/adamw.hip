@@ -338,9 +338,12 @@ __global__ __launch_bounds__(kAdamwThreads) void adamw_kernel(AdamwBatch b, cons
   const int chunk = blockIdx.x;
   AdamwEntry e;
   if (table) {
-    const int which =
-        __builtin_amdgcn_readfirstlane(reinterpret_cast<const int32_t*>(table + (size_t)n * sizeof(AdamwEntry))[chunk]);
-    e = reinterpret_cast<const AdamwEntry*>(table)[which];
+    // a table of another list than the launch's: nothing is done outside it
+    const AdamwTableHead head = *reinterpret_cast<const AdamwTableHead*>(table);
+    if (chunk >= head.chunks || head.entries != n) return;
+    const auto* const entries = reinterpret_cast<const AdamwEntry*>(table + sizeof(AdamwTableHead));
+    const auto* const map = reinterpret_cast<const int32_t*>(entries + n);
+    e = entries[__builtin_amdgcn_readfirstlane(map[chunk])];
   } else {   // the last tensor whose first chunk is not behind this one
     static_assert(kAdamwTensors <= 64, "a tensor a lane");
     const uint64_t begun = __ballot(lane < n && b.t[lane < n ? lane : 0].first <= chunk);

@@ -234,7 +234,7 @@ beam_status_t beam_head_loss_backward(const void* x, const void* w, const int32_
 }
 
 size_t beam_moe_adamw_table_bytes(const beam_adamw_tensor* tensors, int32_t n) {
-  size_t bytes = 16;
+  size_t bytes = sizeof(beam::AdamwTableHead);
   for (int32_t i = 0; tensors && i < n; ++i)
     if (tensors[i].count > 0)
       bytes += sizeof(beam::AdamwEntry) + 4 * (size_t)beam::adamw_chunks(std::min(tensors[i].count, beam::kAdamwMostValues));
@@ -274,7 +274,7 @@ beam_status_t beam_moe_adamw_table(const beam_adamw_tensor* tensors, int32_t n, 
   if (rc != BEAM_OK) return rc;
   size_t used = 0;
   for (int32_t i = 0; i < n; ++i) used += tensors[i].count > 0;
-  char* const entries = reinterpret_cast<char*>(table);
+  char* const entries = reinterpret_cast<char*>(table) + sizeof(beam::AdamwTableHead);
   char* const map = entries + used * sizeof(beam::AdamwEntry);
   int64_t chunks = 0, base = 0;
   int32_t k = 0;
@@ -290,6 +290,9 @@ beam_status_t beam_moe_adamw_table(const beam_adamw_tensor* tensors, int32_t n, 
     base += beam::ceil_div(tensors[i].count, 256);
     ++k;
   }
+  // a list of more chunks than a launch takes is launched without its table
+  const beam::AdamwTableHead head = {k, (int32_t)std::min<int64_t>(chunks, beam::kAdamwMostChunks), {}};
+  std::memcpy(table, &head, sizeof(head));
   return BEAM_OK;
 }
 

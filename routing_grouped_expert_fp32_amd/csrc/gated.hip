@@ -14,6 +14,12 @@
 // rows and a tile of columns. Forward: a tile of BN weight rows takes BN / 2 gate rows and the same BN / 2
 // up rows, in turns of 16, so that a wave holds g and u of the same values. Gradient: the products dh
 // never leave the registers; g and u are read, and d_g, d_u and h written, by its epilogue.
+//
+// Bound by reading the weights for few rows (32 rows, 21 of 32 experts, 5120 -> 2560: 171 us, 6.4 TB/s), by the
+// matrix cores for many (4096 rows of one expert, 5120 -> 20480: 1.39 ms, 1230 TFLOP/s), in between by the weights'
+// latency (8192 rows of 32 experts: 0.47 ms, 4.1 TB/s). The gradient's epilogue moves 10 bytes a value, which little of
+// another tile's arithmetic hides: 32768 skewed rows, 5120 -> 2560, 0.86 ms (matrix cores busy 49%). Fetching its g and
+// u ahead of the products, or two to five sub-tiles ahead, gained nothing.
 #include <type_traits>
 
 #include "row_blocks.h"
@@ -217,7 +223,7 @@ __device__ __forceinline__ void gated_bwd_tile(const GatedBwdArgs& a, const RowB
           return u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
         };
         // both offsets in the lane's register: behind a wide store with a scalar offset the compiler lets the next
-        // instruction write its data registers, and two values in a million came out wrong
+        // instruction write its data registers, and some values in a million came out wrong
         __builtin_amdgcn_raw_buffer_store_b128(packed(dg), dgu_rsrc, off, 0, 0);
         __builtin_amdgcn_raw_buffer_store_b128(packed(du), dgu_rsrc, off + (uint32_t)h_ld, 0, 0);
         __builtin_amdgcn_raw_buffer_store_b128(packed(hv), h_rsrc,
@@ -227,10 +233,8 @@ __device__ __forceinline__ void gated_bwd_tile(const GatedBwdArgs& a, const RowB
           sum = t.in ? sum : 0.f;
 #pragma unroll
           for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor(sum, d);
-          constexpr int kPartLanes = kLanes;   // lanes that could each own a part
-          const int own = (col0 + wn * S::FN * 16) / part_cols, n_own = S::FN * 16 / part_cols;
-          const int k = item % kPartLanes;
-          if (k < n_own && t.m < rows && (item < kItems) && (own + k) * part_cols < a.F)
+          const int own = (col0 + wn * S::FN * 16) / part_cols, n_own = S::FN * 16 / part_cols, k = item % kLanes;
+          if (k < n_own && t.m < rows && item < kItems && (own + k) * part_cols < a.F)
             a.parts[(int64_t)(own + k) * a.R + blk.row0 + t.m] = k == 0 ? sum : 0.f;
         }
       }

@@ -15,8 +15,9 @@
 // roundings are independent from value to value. (Against 64 bits, T = 1: dx 3.9e-3 at worst without, 1.7e-3
 // with it, which is the last rounding's.)
 //
-// Bound by the matrix cores, three products of T x V x H with the loss's as a fourth; for few tokens by
-// reading w (twice for the gradient) and writing dw.
+// Bound by the matrix cores, three products of T x V x H with the loss's as a fourth (4096 tokens, 131072 x 5120: loss
+// 4.43 ms, 1240 TFLOP/s, gradient 13.2 ms, 1250); for few tokens by reading w (32 tokens: loss 200 us, 6.7 TB/s), twice
+// for the gradient, and writing dw.
 #include <cmath>
 #include <type_traits>
 
@@ -55,7 +56,7 @@ __device__ __forceinline__ void logit_tile(const LogitArgs& a, const RowBlock& b
   const int64_t ld = (int64_t)a.H * 2;
   OperandLoader<S::BM, S::kWaves, false> la;
   OperandLoader<S::BN, S::kWaves, false> lb;
-  lb.stream = blk.n_blocks == 1 && !GRAD;
+  lb.stream = blk.n_blocks == 1 && !GRAD;   // the gradient reads these rows of w again for dx
   const int cols = a.V - col0;   // of the piece; the pitch may reach further
   la.init({a.x + blk.row0 * ld, ld, blk.rows, 0}, wave, lane);
   lb.init({a.w + (cols > 0 ? col0 * ld : 0), ld, clamped(cols, 0, S::BN), 0}, wave, lane);

@@ -66,7 +66,9 @@ HeadLayout head_layout(int64_t T, int64_t V, int64_t H) {
 
 HeadBwdLayout head_bwd_layout(int64_t T, int64_t V, int64_t H) {
   HeadBwdLayout L;
-  const int64_t most = std::max<int64_t>(512, kHeadPieceBytes / (2 * std::max<int64_t>(T, 1)) / 256 * 256);
+  const int64_t column = 2 * std::max<int64_t>(T, 1);   // bytes of dz
+  const int64_t most = std::max({kHeadLeastCols, kHeadPieceBytes / column / 256 * 256,
+                                 std::min(kHeadPieceCols, kHeadMostBytes / column / 256 * 256)});
   L.pieces = ceil_div(V, most);
   L.cols = L.pieces == 1 ? V : ceil_div(ceil_div(V, L.pieces), 256) * 256;
   L.pieces = ceil_div(V, L.cols);

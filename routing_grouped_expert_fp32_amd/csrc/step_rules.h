@@ -8,8 +8,11 @@ namespace beam {
 
 // ---- gated products grouped by expert ----
 // A tile's columns are half gate, half up, in sub-tiles of 16 in turn, so each wave needs an even
-// number of them: every tile of the grouped products but the 32 x 64 one. The products' rule, over the
-// 2 F rows of the weights.
+// number of them: every tile of the grouped products but the 32 x 64 one. The products' rule (train_rules.h), over
+// the 2 F rows of the weights. Measured (us) 32 x 128, 64 x 64, 128 x 128, then 128, 192, 256, 320 x 256, the rule's
+// choice last: 32 experts of 5120 -> 2560, 32 rows in all 181, 175, 181, 174, 181, 195, 233: 181; 2048 rows 472, 455,
+// 348, 302, 310, 327, 367: 307; 8192 rows 1304, 988, 670, 591, 549, 520, 423 to 517: the last; 279 rows of one expert, 4152 ->
+// 1056: 27, 25, 50, 41, 54, 60, 92: 25. Over 27 random calls the rule's choice took 6% more than the best tile.
 template <class S>
 constexpr int kGatedCols = S::BN / 2;
 template <class F>
@@ -19,7 +22,10 @@ void with_gated_tile(int64_t R, int64_t E, int64_t Fw, int64_t K, bool keep, F&&
              Tile256Deep{}, Tile320{});
 }
 
-// The gradient's tiles: F columns, contraction over the hidden width; 10 bytes a value beside dy.
+// The gradient's tiles: F columns, contraction over the hidden width; 10 bytes a value beside dy. Measured as above,
+// 32 x 64 second: 32 experts of 5120 -> 2560, 2048 rows 257, 361, 258, 211, 171, 175, 185, 215: 175; 32768 rows 2136,
+// 4024, 1881, 1121, 1102, 1002, 975, 899: 899; 9 rows of 9 experts, 4688 -> 624: 30, 25, 29, 59, 38, 42, 61, 71: 25.
+// Over 18 random calls 3% more than the best tile.
 template <class F>
 void with_gated_bwd_tile(int64_t R, int64_t E, int64_t Fw, int64_t H, F&& f) {
   const RowsCall call(R, E, Fw, H, R * (Fw * 10e-6));
@@ -34,7 +40,10 @@ inline int64_t gated_scale_parts(int64_t Fw) { return ceil_div(Fw, kLeastScaleCo
 
 // ---- loss of the output head ----
 // Logits: the grouped products' rule for one expert of V columns, by tile shape; `store`: their gradient is
-// stored, in bf16.
+// stored, in bf16. Measured (us, the loss, tiles as for the gated products, the rule's choice last): one token, 131072 x
+// 5120: 208, 222, 213, 197, 197, 205, 269: 208; 755 tokens, 23413 x 3624: 369, 284, 198, 172, 146, 171, 177: 154;
+// 2499, 39407 x 2784: 1240, 944, 603, 625, 571, 539, 478: 478; the gradient's logits of 154, 72560 x 720: 59, 46, 43,
+// 45, 39, 40, 41: 39. Over 16 random calls of the loss 8% more than the best tile.
 template <class F>
 void with_head_tile(int64_t T, int64_t V, int64_t H, bool store, F&& f) {
   const RowsCall call(T, 1, V, H, store ? T * (V * 2e-6) : 0.0);
@@ -48,8 +57,12 @@ int64_t head_slots(int64_t V) {
 }
 
 // Gradient of x: tiles of T x H, the contraction over a piece of the vocabulary cut into `parts` runs of
-// `kp` values (whole stages), each with FP32 sums of its own that are added in order. Per tile shape, us: its
-// ends and a stage where the GPU is full.
+// `kp` values (whole stages), each with FP32 sums of its own that are added in order: by a model of the time (full
+// rounds of workgroups, a tile's ends and stages, the sums' traffic). Measured (us, with the addition): 154 x 720, 72560
+// columns: 128 x 128 in 43 parts 35, in 21 41, 256 x 256 in 85 39, 64 x 64 in 43 46, 32 x 128 in 17 44; 2048 x 4096,
+// 65536: 256 x 256 in 2 parts 868, in 1 1470, in 4 922, 128 x 128 in 1 1013; 256 x 5120, 131072: 256 x 256 in 12
+// parts 368, in 13 (a second round) 580; 9 x 2264, 15625: 64 x 64 in 21 parts 15.6, 32 x 128 in 14 15.9, 128 x 128 in
+// 28 16.5.
 struct HeadDxPlan {
   int side;       // tile: 256, 128 or 64 square, 32: 32 x 128
   int parts;
@@ -75,13 +88,20 @@ struct HeadBwdLayout {
   size_t c = 0, xc = 0, sums = 0, total = 0;
   bool direct() const { return pieces == 1 && dx.parts == 1; }
 };
-constexpr int64_t kHeadPieceBytes = int64_t(512) << 20;
+// Columns of a piece: what 512 MiB of dz hold, but 32768 where 4 GiB do (each piece reads and writes T x H sums of dx,
+// 8 bytes against 2 columns' products: 3% of a piece of 32768), and never under 512. 4096 tokens, 131072 x 5120, in
+// pieces of 256 MiB, 512 MiB, 1 GiB: 13.5, 13.3, 13.25 ms.
+constexpr int64_t kHeadPieceBytes = int64_t(512) << 20, kHeadMostBytes = int64_t(4) << 30;
+constexpr int64_t kHeadPieceCols = 32768, kHeadLeastCols = 512;
 HeadBwdLayout head_bwd_layout(int64_t T, int64_t V, int64_t H);
 bool head_grid_fits(int64_t T, int64_t V, int64_t H);
 
 // ---- AdamW step ----
 // A workgroup's chunk: kAdamwUnroll blocks of 256 values a wave. Tensors of a launch without a table: what the
-// kernel's arguments (4 KB) hold. A table: an entry for each tensor that has values, then each chunk's entry.
+// kernel's arguments (4 KB) hold. A table: its head, an entry for each tensor that has values, each chunk's entry.
+struct AdamwTableHead {
+  int32_t entries, chunks, unused[2];
+};
 struct AdamwEntry {
   AdamwTensor t;
   int32_t first;     // its first chunk

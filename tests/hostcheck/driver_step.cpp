@@ -112,7 +112,10 @@ void head_calls(int64_t T, int64_t V, int32_t H, int32_t dt) {
     expect(L.cols * L.pieces >= V && L.cols * (L.pieces - 1) < V && L.pitch % 64 == 0 && L.pitch >= L.cols &&
                (L.pieces == 1 || L.cols % 256 == 0),
            "pieces", T, V, H, L.pieces);
-    expect(2 * T * L.pitch <= beam::kHeadPieceBytes + 2 * T * 256 || L.cols <= 512, "a piece's size", T, V, H, L.cols);
+    const int64_t dz = 2 * T * L.pitch, slack = 2 * T * 256;   // columns go by 256
+    expect(dz <= beam::kHeadPieceBytes + slack || (L.cols <= beam::kHeadPieceCols && dz <= beam::kHeadMostBytes + slack) ||
+               L.cols <= beam::kHeadLeastCols,
+           "a piece's size", T, V, H, L.cols);
     expect(L.dx.kp % 64 == 0 && L.dx.kp * L.dx.parts >= L.cols && L.dx.kp * (L.dx.parts - 1) < L.cols, "parts", T, V, H,
            L.dx.parts);
     const int64_t bm = L.dx.side, bn = L.dx.side == 32 ? 128 : L.dx.side;
@@ -148,20 +151,27 @@ void adamw_calls(int n, int32_t p, int32_t g, int32_t s, bool copy) {
   // every chunk's entry, and the blocks before it
   int32_t used = 0;
   for (auto& a : t) used += a.count > 0;
+  const size_t kHead = sizeof(beam::AdamwTableHead);
   int64_t chunk = 0, blocks = 0;
   int32_t k = 0;
   for (auto& a : t) {
     if (a.count == 0) continue;
     beam::AdamwEntry e;
-    std::memcpy(&e, table.data() + k * sizeof(e), sizeof(e));
+    std::memcpy(&e, table.data() + kHead + k * sizeof(e), sizeof(e));
     expect(e.t.param == a.param && e.t.count == a.count && e.first == chunk && e.base256 == blocks, "an entry", n, k);
     for (int64_t c = 0; c < beam::adamw_chunks(a.count); ++c, ++chunk) {
       int32_t at;
-      std::memcpy(&at, table.data() + used * sizeof(e) + 4 * chunk, 4);
+      std::memcpy(&at, table.data() + kHead + used * sizeof(e) + 4 * chunk, 4);
       expect(at == k, "a chunk's entry", n, k, chunk);
     }
     blocks += ceil_div(a.count, 256);
     ++k;
+  }
+  if (n > 0) {
+    beam::AdamwTableHead head;
+    std::memcpy(&head, table.data(), sizeof(head));
+    expect(head.entries == used && head.chunks == chunk && kHead + used * sizeof(beam::AdamwEntry) + 4 * chunk == table.size(),
+           "the table's head", n);
   }
   void* on_device = buf(table.size(), "table");
   expect(beam_moe_adamw(t.data(), n, p, g, s, &cfg, nullptr, nullptr) == BEAM_OK, "adamw", n);

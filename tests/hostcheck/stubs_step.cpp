@@ -97,7 +97,7 @@ hipError_t launch_adamw(const AdamwTensor* t, int n, const void* table, bool p_b
   const char* l = "adamw";
   size_t entries = 0, chunks = 0;
   for (int i = 0; i < n; ++i) entries += t[i].count > 0, chunks += adamw_chunks(t[i].count);
-  if (table) need(l, "table", table, entries * sizeof(AdamwEntry) + 4 * chunks);
+  if (table) need(l, "table", table, sizeof(AdamwTableHead) + entries * sizeof(AdamwEntry) + 4 * chunks);
   for (int i = 0; i < n; ++i) {
     const size_t c = (size_t)t[i].count, blocks = 4 * ((c + 255) / 256);
     if (c == 0) continue;

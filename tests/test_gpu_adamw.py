@@ -138,6 +138,26 @@ def test_other_gradients():
     _check(t, d, False, False, 2)
 
 
+def test_table_of_another_list():
+    """A table that does not fit the list: one of another number of tensors does nothing, one of fewer values only
+    what it holds. No access is outside either."""
+    t = _state([5000, 300], "f32", "f32", False, False)
+    plan, d = _plan(t, False, False)
+    three, _ = _plan(_state([5000, 300, 20], "f32", "f32", False, False), False, False)
+    big, held = _plan(_state([50000, 70000], "f32", "f32", False, False), False, False)
+    before = [x.clone() for x in d["p"]]
+    own, plan.on_device = plan.on_device, three.on_device
+    bm.adamw(plan, 2, lr=LR)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(before, d["p"]))
+    big_before = [x.clone() for x in held["p"]]
+    big.on_device = own
+    bm.adamw(big, 3, lr=LR, betas=(B1, B2), eps=EPS, weight_decay=WD)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(big_before, held["p"]))
+    _check(t, d, False, False, 3)
+
+
 def test_first_step_from_zeros_and_zero_gradients():
     for eight in (False, True):
         n = 777

@@ -180,8 +180,8 @@ def test_backward_against_differences():
 
 def test_pieces_of_the_vocabulary():
     """A batch whose dz exceeds one piece: several pieces, the last one shorter (dw written by all of them)."""
-    T, V, H = 20000, 20011, 64
-    assert bm.head_loss_backward_workspace_bytes(T, V, H) < 2 * T * V
+    T, V, H = 40000, 70001, 64
+    assert bm.head_loss_backward_workspace_bytes(T, V, H) < T * V
     gen = torch.Generator(device="cuda").manual_seed(1)
     x = torch.randn(T, H, generator=gen, device="cuda").to(BF)
     w = (0.3 * torch.randn(V, H, generator=gen, device="cuda")).to(BF)

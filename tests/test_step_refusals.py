@@ -92,7 +92,7 @@ def test_head_no_tokens_and_sizes():
     assert _hbwd(T=0, dw=None) == NULL and _hbwd(dt=bm.BEAM_FP8_E4M3) == DTYPE
     assert bm.head_loss_workspace_bytes(0, 500, 64) == 0 and bm.head_loss_backward_workspace_bytes(10, 500, 60) == 0
     # the gradient's workspace stays bounded in the vocabulary: no logits
-    assert bm.head_loss_backward_workspace_bytes(65536, 131072, 5120) < 4 * (1 << 30)
+    assert bm.head_loss_backward_workspace_bytes(65536, 131072, 5120) < 7 * (1 << 30)   # dz 4, dx 1.3, x 0.7
     assert bm.head_loss_workspace_bytes(4096, 131072, 5120) < 64 << 20
 
 
