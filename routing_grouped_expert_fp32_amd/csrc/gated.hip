@@ -34,6 +34,16 @@ __device__ __forceinline__ float sigmoid_fast(float g) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g * -1.442695041f));
 }
 
+// silu(g) u of four values, from the FP32 products or from their bf16 roundings gb, ub.
+__device__ __forceinline__ floatx4 gated_values(const floatx4 g, const floatx4 u, u32x2 gb, u32x2 ub, bool rounded) {
+  const floatx4 gv = rounded ? floatx4{bf16_lo(gb.x), bf16_hi(gb.x), bf16_lo(gb.y), bf16_hi(gb.y)} : g;
+  const floatx4 uv = rounded ? floatx4{bf16_lo(ub.x), bf16_hi(ub.x), bf16_lo(ub.y), bf16_hi(ub.y)} : u;
+  floatx4 h;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) h[c] = gv[c] * sigmoid_fast(gv[c]) * uv[c];
+  return h;
+}
+
 // One tile: rows of `blk`, hidden values from col0 on.
 template <class S, bool KEEP>
 __device__ __forceinline__ void gated_tile(const unsigned char* __restrict__ x,
@@ -78,11 +88,7 @@ __device__ __forceinline__ void gated_tile(const unsigned char* __restrict__ x,
         const floatx4 g = acc[i][2 * j], u = acc[i][2 * j + 1];
         const u32x2 gb = {pack_bf16(g.x, g.y), pack_bf16(g.z, g.w)};
         const u32x2 ub = {pack_bf16(u.x, u.y), pack_bf16(u.z, u.w)};
-        const floatx4 gv = rounded ? floatx4{bf16_lo(gb.x), bf16_hi(gb.x), bf16_lo(gb.y), bf16_hi(gb.y)} : g;
-        const floatx4 uv = rounded ? floatx4{bf16_lo(ub.x), bf16_hi(ub.x), bf16_lo(ub.y), bf16_hi(ub.y)} : u;
-        floatx4 hv;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) hv[c] = gv[c] * sigmoid_fast(gv[c]) * uv[c];
+        const floatx4 hv = gated_values(g, u, gb, ub, rounded);
         *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16(hv.x, hv.y), pack_bf16(hv.z, hv.w)};
         if constexpr (KEEP) {
           *reinterpret_cast<u32x2*>(p + kPart) = gb;
@@ -129,6 +135,96 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
     }
   }
   gated_tile<S, KEEP>(x, w, h, gu, blk, col0, F, K, rounded, smem, wave, lane);
+}
+
+// Few rows of few experts: a block's 32 rows (NV sub-tiles of 16) by 16 hidden values a workgroup, the contraction
+// in turns of 64 over its eight waves, whose sums meet in LDS. Fragments go from memory to registers, kNarrowAhead
+// turns of a wave at once: 128 bytes of a weight row a turn, 1 KB by the eight waves.
+template <bool KEEP, int NV>
+__device__ __forceinline__ void gated_narrow_block(const unsigned char* __restrict__ x,
+                                                   const unsigned char* __restrict__ w,
+                                                   unsigned char* __restrict__ h, unsigned char* __restrict__ gu,
+                                                   const RowBlock& blk, int col0, int F, int K, bool rounded,
+                                                   floatx4* red, int wave, int lane) {
+  const int64_t ld = (int64_t)K * 2;
+  const int r = lane & 15, g8 = 8 * (lane >> 4);
+  const unsigned char* const xb = uniform(x + (int64_t)blk.row0 * ld);
+  const unsigned char* const wb = uniform(w + (blk.e * 2 * (int64_t)F + col0) * ld);
+  // rows past the block's, and weight rows past the up ones, are past their buffers and read as zero; gate rows past
+  // the last are up rows, whose sums are dropped
+  const uint32_t x_bytes = (uint32_t)(blk.rows * ld), w_bytes = (uint32_t)((2 * F - col0) * ld);
+  const uint32_t x_row = (uint32_t)(r * ld), up = (uint32_t)(F * ld);
+  floatx4 acc[NV][2];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) acc[i][0] = acc[i][1] = floatx4{0.f, 0.f, 0.f, 0.f};
+  const int turns = (K + 63) >> 6;
+  for (int t0 = wave; t0 < turns; t0 += kNarrowWaves * kNarrowAhead) {
+    intx4 wf[kNarrowAhead][2][2], xf[kNarrowAhead][2][NV];
+#pragma unroll
+    for (int a = 0; a < kNarrowAhead; ++a)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int k = 64 * (t0 + kNarrowWaves * a) + 32 * s + g8;
+        const uint32_t at = x_row + 2 * (uint32_t)k, past = k < K ? 0u : 0x80000000u;
+        wf[a][s][0] = __builtin_bit_cast(intx4, buffer_load16<0>(wb, w_bytes, at | past, 0));
+        wf[a][s][1] = __builtin_bit_cast(intx4, buffer_load16<0>(wb, w_bytes, (at + up) | past, 0));
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          xf[a][s][i] =
+              __builtin_bit_cast(intx4, buffer_load16<0>(xb, x_bytes, (at + (uint32_t)(16 * i * ld)) | past, 0));
+      }
+    __builtin_amdgcn_sched_barrier(0);   // all of them before the first product
+#pragma unroll
+    for (int a = 0; a < kNarrowAhead; ++a)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int p = 0; p < 2; ++p) acc[i][p] = tile_mma<false>(wf[a][s][p], xf[a][s][i], acc[i][p]);
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) red[((i * 2 + p) * kNarrowWaves + wave) * 64 + lane] = acc[i][p];
+  __syncthreads();
+  if (wave >= NV) return;
+  floatx4 v[2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const floatx4* const mine = red + (wave * 2 + p) * kNarrowWaves * 64 + lane;
+    v[p] = mine[0];
+#pragma unroll
+    for (int k = 1; k < kNarrowWaves; ++k) v[p] += mine[k * 64];
+  }
+  const int m = 16 * wave + r, n = col0 + g8 / 2;   // a lane's four values of a row
+  if (m >= blk.rows || n >= F) return;
+  const u32x2 gb = {pack_bf16(v[0].x, v[0].y), pack_bf16(v[0].z, v[0].w)};
+  const u32x2 ub = {pack_bf16(v[1].x, v[1].y), pack_bf16(v[1].z, v[1].w)};
+  const floatx4 hv = gated_values(v[0], v[1], gb, ub, rounded);
+  const int64_t row = blk.row0 + m;
+  *reinterpret_cast<u32x2*>(h + (row * F + n) * 2) = u32x2{pack_bf16(hv.x, hv.y), pack_bf16(hv.z, hv.w)};
+  if constexpr (KEEP) {
+    *reinterpret_cast<u32x2*>(gu + (row * 2 * F + n) * 2) = gb;
+    *reinterpret_cast<u32x2*>(gu + (row * 2 * F + F + n) * 2) = ub;
+  }
+}
+
+template <bool KEEP>
+__global__ __launch_bounds__(64 * kNarrowWaves, 2) void gated_narrow_kernel(
+    const unsigned char* __restrict__ x, const unsigned char* __restrict__ w,
+    const int32_t* __restrict__ offsets, unsigned char* __restrict__ h, unsigned char* __restrict__ gu, int R,
+    int E, int F, int K, bool rounded, int n_ctiles, int max_blocks) {
+  __shared__ floatx4 red[2 * 2 * kNarrowWaves * 64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  RowBlock blk;
+  int ctile, half;
+  if (!row_block_tile<TileStream, true>(offsets, R, E, n_ctiles, max_blocks, lane, blk, ctile, half)) return;
+  if (blk.rows > 16)
+    gated_narrow_block<KEEP, 2>(x, w, h, gu, blk, ctile * kNarrowCols, F, K, rounded, red, wave, lane);
+  else
+    gated_narrow_block<KEEP, 1>(x, w, h, gu, blk, ctile * kNarrowCols, F, K, rounded, red, wave, lane);
 }
 
 struct GatedBwdArgs {
@@ -277,6 +373,19 @@ __global__ __launch_bounds__(256) void gated_scale_kernel(const float* __restric
 
 hipError_t launch_gated(const void* x, const void* w, const int32_t* offsets, void* h, void* gu, int R, int E,
                         int F, int K, bool rounded, hipStream_t st) {
+  if (gated_is_narrow(R, E, F, K)) {
+    const int64_t blocks = grouped_max_blocks(R, E, TileStream::BM);
+    const int n_ctiles = (int)ceil_div(F, kNarrowCols);
+    const dim3 grid((unsigned)xcd_workgroups_halves<TileStream>(blocks * n_ctiles));
+    auto go = [&](auto keep) {
+      hipLaunchKernelGGL((gated_narrow_kernel<decltype(keep)::value>), grid, dim3(64 * kNarrowWaves), 0, st,
+                         reinterpret_cast<const unsigned char*>(x), reinterpret_cast<const unsigned char*>(w),
+                         offsets, reinterpret_cast<unsigned char*>(h), reinterpret_cast<unsigned char*>(gu), R,
+                         E, F, K, rounded, n_ctiles, (int)blocks);
+    };
+    gu ? go(std::true_type{}) : go(std::false_type{});
+    return hipGetLastError();
+  }
   with_gated_tile(R, E, F, K, gu != nullptr, [&](auto s) {
     using S = decltype(s);
     const int64_t blocks = grouped_max_blocks(R, E, S::BM);

@@ -3,6 +3,14 @@
 
 namespace beam {
 
+bool gated_is_narrow(int64_t R, int64_t E, int64_t Fw, int64_t K) {
+  const double full = (double)std::min(R, E), mean = (double)R / full;
+  const double blocks = E == 1                                      ? std::ceil(mean / 32)
+                        : mean + 2.5 * std::sqrt(mean) <= 32.0 ? 1.0
+                                                                    : mean / 32 + 0.5;
+  return K >= 1280 && full * blocks * ceil_div(Fw, kNarrowCols) <= 1.5 * kGroupedCus;
+}
+
 bool gated_grid_fits(int64_t R, int64_t E, int64_t Fw, int64_t K) {
   // the narrowest tiles' launch fits: so does any
   if (threads_fit<Tile256>(grouped_max_blocks(R, E, 32) * ceil_div(Fw, 32))) return true;

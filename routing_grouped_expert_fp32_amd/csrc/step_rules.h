@@ -22,6 +22,16 @@ void with_gated_tile(int64_t R, int64_t E, int64_t Fw, int64_t K, bool keep, F&&
              Tile256Deep{}, Tile320{});
 }
 
+// Few rows of few experts make few tiles, each a chain of stages: blocks of 32 rows by kNarrowCols hidden values instead,
+// the contraction split over a workgroup's waves, where those are at most one and a half a CU and the chain is long.
+// Measured (us, the tiles first): one row, 5120 -> 2560, 160 blocks, 30.3, 13.6; 8 rows, 4624 -> 944, 59: 22.5, 10.8; 4
+// rows, 4096 -> 4096, 256: 25.8, 14.7; one row each of 4 experts, 5120 -> 2560, 320 to 480: 32.2, 26.5; 16 rows, 4096 ->
+// 8192, 512: 29.5, 29.9; 20 rows of 16 experts, 2048 -> 704, 528: 15.9, 21.5; 128 rows, 4096 -> 1024, 256: 23.9, 19.5; 16
+// rows, 2048 -> 1024, 64: 11.5, 8.7; 30 rows, 1024 -> 2560, 160: 8.1, 8.2. Turns of a wave at once: five; with eight
+// these are 15.7, 12.8 and 13.4 (fewer of them past the end of most contractions).
+constexpr int kNarrowWaves = 8, kNarrowAhead = 5, kNarrowCols = 16;
+bool gated_is_narrow(int64_t R, int64_t E, int64_t Fw, int64_t K);
+
 // The gradient's tiles: F columns, contraction over the hidden width; 10 bytes a value beside dy. Measured as above,
 // 32 x 64 second: 32 experts of 5120 -> 2560, 2048 rows 257, 361, 258, 211, 171, 175, 185, 215: 175; 32768 rows 2136,
 // 4024, 1881, 1121, 1102, 1002, 975, 899: 899; 9 rows of 9 experts, 4688 -> 624: 30, 25, 29, 59, 38, 42, 61, 71: 25.

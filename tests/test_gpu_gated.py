@@ -98,6 +98,21 @@ def test_forward_every_tile(counts):
     check_forward(counts, 1288, 72, True, False)
 
 
+@pytest.mark.parametrize("rounded", [False, True])
+@pytest.mark.parametrize("keep", [False, True])
+@pytest.mark.parametrize("counts,F,K", [([1], 8, 1280), ([1], 2560, 1288), ([16], 24, 5120), ([17], 40, 1352),
+                                        ([32], 264, 2048), ([33], 136, 1344), ([100], 72, 4104), ([7, 0, 1], 520, 1600),
+                                        ([3] * 20, 16, 1280), ([0, 0, 30], 1000, 1296), ([90, 2, 0, 40], 56, 1280)])
+def test_forward_few_rows(counts, F, K, keep, rounded):
+    """Sizes that split the contraction over a workgroup's waves."""
+    check_forward(counts, F, K, keep, rounded)
+
+
+def test_forward_few_rows_of_no_expert():
+    check_forward([5, 0, 9], 40, 1288, True, False, first=3, behind=4)
+    check_forward([0] * 70 + [2] + [0] * 60 + [19], 24, 1280, True, True)
+
+
 def check_backward(counts, F, H, scaled, first=0, behind=0, seed=1, spread=1.4):
     print("gated backward", counts[:8], len(counts), F, H, scaled, flush=True)
     off = _offsets(counts, first)
@@ -253,7 +268,12 @@ def test_offsets_out_of_order_are_harmless():
     gen = torch.Generator().manual_seed(4)
     x, w = _randn(gen, R, K).cuda(), _randn(gen, 3, 2 * F, K).cuda()
     dy, wd, s = _randn(gen, R, K).cuda(), _randn(gen, 3, K, F).cuda(), torch.rand(R).cuda()
+    xk, wk = _randn(gen, R, 1280).cuda(), _randn(gen, 3, 2 * F, 1280).cuda()
     for off in ([0, 60, -5, 50], [50, 20, 30, 0], [-9, -3, 2 ** 31 - 1, 7]):
+        long = torch.full((R + 32, F), 3.0, dtype=BF, device="cuda")
+        bm.gated_mm(xk, wk, torch.tensor(off, dtype=torch.int32, device="cuda"), keep=True, h=long[16:16 + R])
+        torch.cuda.synchronize()
+        assert (long[:16] == 3).all() and (long[16 + R:] == 3).all()
         room = torch.full((R + 32, F), 3.0, dtype=BF, device="cuda")
         offs = torch.tensor(off, dtype=torch.int32, device="cuda")
         _, gu = bm.gated_mm(x, w, offs, keep=True, h=room[16:16 + R])
