@@ -22,6 +22,7 @@
 // u ahead of the products, or two to five sub-tiles ahead, gained nothing.
 #include <type_traits>
 
+#include "narrow.h"
 #include "row_blocks.h"
 #include "step_rules.h"
 
@@ -137,9 +138,7 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
   gated_tile<S, KEEP>(x, w, h, gu, blk, col0, F, K, rounded, smem, wave, lane);
 }
 
-// Few rows of few experts: a block's 32 rows (NV sub-tiles of 16) by 16 hidden values a workgroup, the contraction
-// in turns of 64 over its eight waves, whose sums meet in LDS. Fragments go from memory to registers, kNarrowAhead
-// turns of a wave at once: 128 bytes of a weight row a turn, 1 KB by the eight waves.
+// Few rows of few experts: a block's 32 rows (NV sub-tiles of 16) by 16 hidden values a workgroup (narrow.h).
 template <bool KEEP, int NV>
 __device__ __forceinline__ void gated_narrow_block(const unsigned char* __restrict__ x,
                                                    const unsigned char* __restrict__ w,
@@ -147,57 +146,13 @@ __device__ __forceinline__ void gated_narrow_block(const unsigned char* __restri
                                                    const RowBlock& blk, int col0, int F, int K, bool rounded,
                                                    floatx4* red, int wave, int lane) {
   const int64_t ld = (int64_t)K * 2;
-  const int r = lane & 15, g8 = 8 * (lane >> 4);
-  const unsigned char* const xb = uniform(x + (int64_t)blk.row0 * ld);
-  const unsigned char* const wb = uniform(w + (blk.e * 2 * (int64_t)F + col0) * ld);
-  // rows past the block's, and weight rows past the up ones, are past their buffers and read as zero; gate rows past
-  // the last are up rows, whose sums are dropped
-  const uint32_t x_bytes = (uint32_t)(blk.rows * ld), w_bytes = (uint32_t)((2 * F - col0) * ld);
-  const uint32_t x_row = (uint32_t)(r * ld), up = (uint32_t)(F * ld);
-  floatx4 acc[NV][2];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) acc[i][0] = acc[i][1] = floatx4{0.f, 0.f, 0.f, 0.f};
-  const int turns = (K + 63) >> 6;
-  for (int t0 = wave; t0 < turns; t0 += kNarrowWaves * kNarrowAhead) {
-    intx4 wf[kNarrowAhead][2][2], xf[kNarrowAhead][2][NV];
-#pragma unroll
-    for (int a = 0; a < kNarrowAhead; ++a)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int k = 64 * (t0 + kNarrowWaves * a) + 32 * s + g8;
-        const uint32_t at = x_row + 2 * (uint32_t)k, past = k < K ? 0u : 0x80000000u;
-        wf[a][s][0] = __builtin_bit_cast(intx4, buffer_load16<0>(wb, w_bytes, at | past, 0));
-        wf[a][s][1] = __builtin_bit_cast(intx4, buffer_load16<0>(wb, w_bytes, (at + up) | past, 0));
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-          xf[a][s][i] =
-              __builtin_bit_cast(intx4, buffer_load16<0>(xb, x_bytes, (at + (uint32_t)(16 * i * ld)) | past, 0));
-      }
-    __builtin_amdgcn_sched_barrier(0);   // all of them before the first product
-#pragma unroll
-    for (int a = 0; a < kNarrowAhead; ++a)
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-          for (int p = 0; p < 2; ++p) acc[i][p] = tile_mma<false>(wf[a][s][p], xf[a][s][i], acc[i][p]);
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int p = 0; p < 2; ++p) red[((i * 2 + p) * kNarrowWaves + wave) * 64 + lane] = acc[i][p];
-  __syncthreads();
-  if (wave >= NV) return;
   floatx4 v[2];
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const floatx4* const mine = red + (wave * 2 + p) * kNarrowWaves * 64 + lane;
-    v[p] = mine[0];
-#pragma unroll
-    for (int k = 1; k < kNarrowWaves; ++k) v[p] += mine[k * 64];
-  }
-  const int m = 16 * wave + r, n = col0 + g8 / 2;   // a lane's four values of a row
+  // weight rows past the up ones read as zero; gate rows past the last are up rows, whose sums are dropped
+  if (!narrow_products<NV>(x + (int64_t)blk.row0 * ld, (uint32_t)(blk.rows * ld),
+                           w + (blk.e * 2 * (int64_t)F + col0) * ld, (uint32_t)((2 * F - col0) * ld),
+                           (uint32_t)(F * ld), K, red, wave, lane, v))
+    return;
+  const int m = 16 * wave + (lane & 15), n = col0 + 4 * (lane >> 4);
   if (m >= blk.rows || n >= F) return;
   const u32x2 gb = {pack_bf16(v[0].x, v[0].y), pack_bf16(v[0].z, v[0].w)};
   const u32x2 ub = {pack_bf16(v[1].x, v[1].y), pack_bf16(v[1].z, v[1].w)};
@@ -215,7 +170,7 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void gated_narrow_kernel(
     const unsigned char* __restrict__ x, const unsigned char* __restrict__ w,
     const int32_t* __restrict__ offsets, unsigned char* __restrict__ h, unsigned char* __restrict__ gu, int R,
     int E, int F, int K, bool rounded, int n_ctiles, int max_blocks) {
-  __shared__ floatx4 red[2 * 2 * kNarrowWaves * 64];
+  __shared__ floatx4 red[kNarrowSums];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   RowBlock blk;

@@ -21,6 +21,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "narrow.h"
 #include "row_blocks.h"
 #include "step_rules.h"
 
@@ -48,8 +49,63 @@ struct LogitArgs {
   int pitch;
 };
 
-// FP32 logits of a tile in its accumulators, and what the launch makes of them: with GRAD q, zero from V
-// to the pitch, else the rows' maxima and sums in column slot `slot`.
+// What a launch makes of 4 N FP32 logits z of a row that a lane has, columns n0 + 16 j + 0..3 of a tile of `cols`: with
+// GRAD q, zero past the columns, else the row's maximum and sum of exponentials over the lanes that share it (16 and
+// 32 apart). `in`: the row m of the block exists.
+template <bool GRAD, bool CAP, int N>
+__device__ __forceinline__ float2 logit_row(const LogitArgs& a, floatx4 (&z4)[N], int row0, int m, bool in, int col0,
+                                            int n0, int cols) {
+  const float inv_cap = CAP ? 1.f / a.cap : 0.f;
+  const int t = row0 + (in ? m : 0);
+  const int y = a.targets[t] - a.v0 - col0;   // the target's column of this tile, if it has one
+  if constexpr (GRAD) {
+    const float lse = a.lse[t], inv = a.inv_c[t];
+    const bool counts = in && inv != 0.f;   // a row without a loss may hold anything
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int n = n0 + 16 * j + c;
+        float z = z4[j][c], slope = 1.f;
+        if constexpr (CAP) {
+          z = soft_cap(z, a.cap, inv_cap);
+          const float r = z * inv_cap;
+          slope = 1.f - r * r;
+        }
+        const float p = exp_fast(z - lse) - (n == y ? 1.f : 0.f);
+        z4[j][c] = n < cols && counts ? p * slope * inv : 0.f;
+      }
+    return make_float2(0.f, 0.f);
+  } else {
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int n = n0 + 16 * j + c;
+        float z = z4[j][c];
+        if constexpr (CAP) z = soft_cap(z, a.cap, inv_cap);
+        z = n < cols ? z : -INFINITY;
+        z4[j][c] = z;
+        top = fmaxf(top, z);
+        if (in && n == y && n < cols) a.at_target[t] = z;
+      }
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float from = top == -INFINITY ? 0.f : top;   // no column: every term is e^-inf
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) sum += exp_fast(z4[j][c] - from);
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    return make_float2(top, sum);
+  }
+}
+
+// The logits of a tile and what the launch makes of them: q from its columns to the pitch, or the rows' maxima and
+// sums in column slot `slot`.
 template <class S, bool GRAD, bool CAP>
 __device__ __forceinline__ void logit_tile(const LogitArgs& a, const RowBlock& blk, int col0, int slot,
                                            unsigned char* smem, int wave, int lane) {
@@ -63,63 +119,17 @@ __device__ __forceinline__ void logit_tile(const LogitArgs& a, const RowBlock& b
   floatx4 acc[S::FM][S::FN];
   tile_zero<S>(acc);
   const int wm = wave / S::WN, wn = wave % S::WN;
-  const float inv_cap = CAP ? 1.f / a.cap : 0.f;
   float2* const row_sums = reinterpret_cast<float2*>(smem);   // [WN][BM], in the ring that nobody reads any more
   static_assert(S::WN * S::BM * 8 <= S::kLdsBytes, "row sums fit the ring");
   with_row_subtiles<S>(blk.rows, wave, [&](auto nv_tag) {
     constexpr int NV = decltype(nv_tag)::value;
     tile_kloop<S, false, false, false, NV>(la, lb, a.H, smem, wave, lane, acc);
-    const int n0 = wn * S::FN * 16 + 4 * (lane >> 4);   // a lane's columns: n0 + 16 j + c
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int m = 16 * S::row_tile(wm, i) + (lane & 15);
-      const bool in = m < blk.rows;
-      const int t = blk.row0 + (in ? m : 0);
-      const int target = a.targets[t];
-      const int y = target - a.v0 - col0;   // the target's column of this tile, if it has one
-      if constexpr (GRAD) {
-        const float lse = a.lse[t], inv = a.inv_c[t];
-        const bool counts = inv != 0.f;   // a row without a loss may have any lse
-#pragma unroll
-        for (int j = 0; j < S::FN; ++j)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int n = n0 + 16 * j + c;
-            float z = acc[i][j][c], slope = 1.f;
-            if constexpr (CAP) {
-              z = soft_cap(z, a.cap, inv_cap);
-              const float r = z * inv_cap;
-              slope = 1.f - r * r;
-            }
-            const float p = exp_fast(z - lse) - (n == y ? 1.f : 0.f);
-            acc[i][j][c] = n < cols && counts ? p * slope * inv : 0.f;
-          }
-      } else {
-        float top = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < S::FN; ++j)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int n = n0 + 16 * j + c;
-            float z = acc[i][j][c];
-            if constexpr (CAP) z = soft_cap(z, a.cap, inv_cap);
-            z = n < cols ? z : -INFINITY;
-            acc[i][j][c] = z;
-            top = fmaxf(top, z);
-            if (in && n == y && n < cols) a.at_target[t] = z;
-          }
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float from = top == -INFINITY ? 0.f : top;   // no column: every term is e^-inf
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < S::FN; ++j)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) sum += exp_fast(acc[i][j][c] - from);
-        sum += __shfl_xor(sum, 16);
-        sum += __shfl_xor(sum, 32);
-        if (lane < 16) row_sums[wn * S::BM + m] = make_float2(top, sum);
-      }
+      const float2 r = logit_row<GRAD, CAP>(a, acc[i], blk.row0, m, m < blk.rows, col0, wn * S::FN * 16 + 4 * (lane >> 4),
+                                            cols);
+      if (!GRAD && lane < 16) row_sums[wn * S::BM + m] = r;
     }
     if constexpr (GRAD)
       tile_store<S, NV, true>(acc, a.q + ((int64_t)blk.row0 * a.pitch + col0) * 2, (int64_t)a.pitch * 2, blk.rows,
@@ -138,6 +148,43 @@ __device__ __forceinline__ void logit_tile(const LogitArgs& a, const RowBlock& b
       a.stats[(int64_t)slot * a.T + blk.row0 + m] = r;
     }
   }
+}
+
+// The same for few rows and columns: a block of 32 rows by kNarrowLogits columns a workgroup (narrow.h), a slot each.
+template <bool GRAD, bool CAP, int NV>
+__device__ __forceinline__ void logit_narrow_block(const LogitArgs& a, const RowBlock& blk, int ctile, floatx4* red,
+                                                   int wave, int lane) {
+  const int64_t ld = (int64_t)a.H * 2;
+  const int col0 = ctile * kNarrowLogits, cols = a.V - col0;   // none left between V and the pitch
+  floatx4 v[2];
+  if (!narrow_products<NV>(a.x + blk.row0 * ld, (uint32_t)(blk.rows * ld), a.w + (cols > 0 ? col0 * ld : 0),
+                           (uint32_t)(clamped(cols, 0, kNarrowLogits) * ld), (uint32_t)(16 * ld), a.H, red, wave, lane, v))
+    return;
+  const int m = 16 * wave + (lane & 15), n0 = 4 * (lane >> 4);
+  const bool in = m < blk.rows;
+  const float2 r = logit_row<GRAD, CAP>(a, v, blk.row0, m, in, col0, n0, cols);
+  if (!in) return;
+  if constexpr (GRAD) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)   // the pitch is a multiple of 64
+      *reinterpret_cast<u32x2*>(a.q + ((int64_t)(blk.row0 + m) * a.pitch + col0 + n0 + 16 * j) * 2) =
+          u32x2{pack_bf16(v[j].x, v[j].y), pack_bf16(v[j].z, v[j].w)};
+  } else {
+    if (lane < 16) a.stats[(int64_t)ctile * a.T + blk.row0 + m] = r;
+  }
+}
+
+template <bool GRAD, bool CAP>
+__global__ __launch_bounds__(64 * kNarrowWaves, 2) void logit_narrow_kernel(LogitArgs a, int n_ctiles) {
+  __shared__ floatx4 red[kNarrowSums];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  RowBlock blk{0, (int)blockIdx.x / n_ctiles * 32, 0, 0, 0};
+  blk.rows = min(32, a.T - blk.row0);
+  if (blk.rows > 16)
+    logit_narrow_block<GRAD, CAP, 2>(a, blk, blockIdx.x % n_ctiles, red, wave, lane);
+  else
+    logit_narrow_block<GRAD, CAP, 1>(a, blk, blockIdx.x % n_ctiles, red, wave, lane);
 }
 
 // Nothing in column slot `slot`.
@@ -376,6 +423,15 @@ __global__ __launch_bounds__(S::kThreads, S::kLdsBytes <= 80 * 1024 ? 2 : 1) voi
 
 template <bool GRAD>
 void launch_logits(const LogitArgs& a, int64_t end, hipStream_t st) {
+  if (head_is_narrow(a.T, end, a.H)) {
+    const int n_ctiles = (int)ceil_div(end, kNarrowLogits);
+    const dim3 grid((unsigned)(ceil_div(a.T, 32) * n_ctiles));
+    if (a.cap > 0.f)
+      hipLaunchKernelGGL((logit_narrow_kernel<GRAD, true>), grid, dim3(64 * kNarrowWaves), 0, st, a, n_ctiles);
+    else
+      hipLaunchKernelGGL((logit_narrow_kernel<GRAD, false>), grid, dim3(64 * kNarrowWaves), 0, st, a, n_ctiles);
+    return;
+  }
   with_head_tile(a.T, a.V, a.H, GRAD, [&](auto s) {
     using S = decltype(s);
     const int n_ctiles = (int)ceil_div(end, S::BN);

@@ -66,7 +66,10 @@ HeadDxPlan head_dx_plan(int64_t T, int64_t H, int64_t cols) {
 
 HeadLayout head_layout(int64_t T, int64_t V, int64_t H) {
   HeadLayout L;
-  with_head_tile(T, V, H, false, [&](auto s) { L.slots = head_slots<decltype(s)>(V); });
+  if (head_is_narrow(T, V, H))
+    L.slots = ceil_div(V, kNarrowLogits);
+  else
+    with_head_tile(T, V, H, false, [&](auto s) { L.slots = head_slots<decltype(s)>(V); });
   L.at_target = ((size_t)L.slots * (size_t)T * 8 + 255) & ~size_t(255);
   L.total = L.at_target + (((size_t)T * 4 + 255) & ~size_t(255));
   return L;

@@ -60,6 +60,17 @@ void with_head_tile(int64_t T, int64_t V, int64_t H, bool store, F&& f) {
   with_least([&](auto s) { return call.us(s); }, f, TileStream{}, Tile64{}, TilePair{}, Tile128{}, Tile192{},
              Tile256Deep{}, Tile320{});
 }
+// Few tokens and columns (`end` of them, to the pitch for the gradient): blocks of 32 tokens by kNarrowLogits columns
+// as for the gated products, where they are at most one a CU. Measured (us, the loss's logits, then the gradient's, the
+// tiles first): one token, 1000 x 1280, 32 blocks, 8.7, 6.2 and 7.0, 5.6; 2, 300 x 5120, 10: 30.2, 12.6 and 20.9, 12.3;
+// 8, 4096 x 4096, 128: 25.0, 12.7 and 17.3, 13.9; 32 of them 25.2, 17.9 and 17.4, 18.6; 16, 8192 x 5120, 256: 32.7, 18.3
+// and 21.7, 18.3; 32, 8000 x 1600, 250: 12.2, 9.6 and 8.9, 9.9; 128, 2048 x 4096, 256: 24.2, 18.5 and 21.4, 18.4. 384
+// blocks: one, 12288 x 5120 33.8, 26.5 and 22.2, 26.2; 32, 12288 x 2048 15.5, 20.3 and 10.9, 20.6; 64, 6144 x 5120 34.6,
+// 41.6 and 27.0, 41.5.
+constexpr int kNarrowLogits = 32;
+inline bool head_is_narrow(int64_t T, int64_t end, int64_t H) {
+  return H >= 1280 && ceil_div(T, 32) * ceil_div(end, kNarrowLogits) <= kGroupedCus;
+}
 // Column slots of a row's partial sums: one a tile, two where a tile may be split.
 template <class S>
 int64_t head_slots(int64_t V) {
