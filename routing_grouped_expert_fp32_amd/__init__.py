@@ -731,8 +731,9 @@ def head_loss_backward(x, w, targets, lse, d_loss, softcap: float = 0.0, dx=None
 
 class AdamWPlan:
     """The tensors of an AdamW step (adamw_plan), which it holds, and their table, on the host for the C ABI
-    and on the device for the launch."""
-    __slots__ = ("tensors", "table", "grads", "dtypes", "device", "on_device")
+    and on the device for the launch. It may be dropped while steps of it are pending, on whatever stream; a
+    graph that holds a step needs it, and its tensors, as long as it is replayed."""
+    __slots__ = ("tensors", "table", "grads", "dtypes", "device", "on_device", "stream")
 
 
 def _adamw_grads(plan, grads):
@@ -791,8 +792,11 @@ def adamw_plan(params, grads, m, v, m_scales=None, v_scales=None, copies=None) -
     rc = lib().beam_moe_adamw_table(table, n, *plan.dtypes, host.data_ptr(), host.numel())
     if rc != 0:
         raise BeamError(rc, "beam_moe_adamw_table")
-    # from pageable memory: the copy is done when the call returns, whatever stream the steps run on
-    plan.on_device = None if plan.device is None else host.to(torch.device("cuda", plan.device))
+    plan.on_device = plan.stream = None
+    if plan.device is not None:
+        plan.stream = torch._C._cuda_getCurrentRawStream(plan.device)   # the stream that the table's memory belongs to
+        # from pageable memory: the copy is done when the call returns, whatever stream the steps run on
+        plan.on_device = host.to(torch.device("cuda", plan.device))
     return plan
 
 
@@ -828,6 +832,10 @@ def adamw(plan: AdamWPlan, step, lr, betas=(0.9, 0.95), eps: float = 1e-8, weigh
         on_device = None
     ctx, st = _on(plan.device, stream)
     with ctx:
+        if on_device is not None and st != plan.stream:
+            # the launch reads the table on another stream than its own: a plan dropped before it has run must
+            # not hand the memory on
+            plan.on_device.record_stream(torch.cuda.current_stream(plan.device))
         rc = lib().beam_moe_adamw(table, n, *plan.dtypes, ctypes.byref(cfg), on_device, st)
     if rc != 0:
         raise BeamError(rc, "beam_moe_adamw")
