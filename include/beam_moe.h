@@ -430,8 +430,8 @@ BEAM_API size_t beam_head_loss_backward_workspace_bytes(int64_t T, int64_t V, in
  * checks it as a whole (no two arrays may overlap; gradients may share memory) and writes the table to HOST memory
  * of at least beam_moe_adamw_table_bytes(tensors, n); the caller copies it to the device (16-byte aligned) and hands
  * that in with the same list, and the step is one launch. (The table's tensors are what is updated; one of another
- * number of tensors or fewer chunks than the list's does no more than it holds.) device_table = NULL: a launch for
- * every 54 tensors.
+ * number of tensors, or of other types, does nothing, one of fewer values no more than it holds.)
+ * device_table = NULL: a launch for every 54 tensors.
  * Limits: 0 <= beta < 1, 1e-30 <= eps <= 1e30, count under 2^36, fewer than 2^39 values in all. No workspace;
  * n = 0 is a no-op. */
 typedef struct beam_adamw_tensor {

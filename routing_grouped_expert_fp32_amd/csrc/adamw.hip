@@ -338,9 +338,9 @@ __global__ __launch_bounds__(kAdamwThreads) void adamw_kernel(AdamwBatch b, cons
   const int chunk = blockIdx.x;
   AdamwEntry e;
   if (table) {
-    // a table of another list than the launch's: nothing is done outside it
+    // a table of another list than the launch's: nothing is done outside it, and nothing at all to other types
     const AdamwTableHead head = *reinterpret_cast<const AdamwTableHead*>(table);
-    if (chunk >= head.chunks || head.entries != n) return;
+    if (chunk >= head.chunks || head.entries != n || head.types != adamw_types(P_BF16, G_BF16, Q8, COPY)) return;
     const auto* const entries = reinterpret_cast<const AdamwEntry*>(table + sizeof(AdamwTableHead));
     const auto* const map = reinterpret_cast<const int32_t*>(entries + n);
     e = entries[__builtin_amdgcn_readfirstlane(map[chunk])];

@@ -273,7 +273,12 @@ beam_status_t beam_moe_adamw_table(const beam_adamw_tensor* tensors, int32_t n, 
   delete[] all;
   if (rc != BEAM_OK) return rc;
   size_t used = 0;
-  for (int32_t i = 0; i < n; ++i) used += tensors[i].count > 0;
+  bool copies = false;   // of all or of none
+  for (int32_t i = 0; i < n; ++i) {
+    if (tensors[i].count == 0) continue;
+    ++used;
+    copies = tensors[i].copy != nullptr;
+  }
   char* const entries = reinterpret_cast<char*>(table) + sizeof(beam::AdamwTableHead);
   char* const map = entries + used * sizeof(beam::AdamwEntry);
   int64_t chunks = 0, base = 0;
@@ -291,7 +296,9 @@ beam_status_t beam_moe_adamw_table(const beam_adamw_tensor* tensors, int32_t n, 
     ++k;
   }
   // a list of more chunks than a launch takes is launched without its table
-  const beam::AdamwTableHead head = {k, (int32_t)std::min<int64_t>(chunks, beam::kAdamwMostChunks), {}};
+  const beam::AdamwTableHead head = {
+      k, (int32_t)std::min<int64_t>(chunks, beam::kAdamwMostChunks),
+      beam::adamw_types(param_dtype == BEAM_BF16, grad_dtype == BEAM_BF16, state_dtype == BEAM_FP8_E4M3, copies), 0};
   std::memcpy(table, &head, sizeof(head));
   return BEAM_OK;
 }

@@ -121,8 +121,12 @@ bool head_grid_fits(int64_t T, int64_t V, int64_t H);
 // A workgroup's chunk: kAdamwUnroll blocks of 256 values a wave. Tensors of a launch without a table: what the
 // kernel's arguments (4 KB) hold. A table: its head, an entry for each tensor that has values, each chunk's entry.
 struct AdamwTableHead {
-  int32_t entries, chunks, unused[2];
+  int32_t entries, chunks, types, unused;   // types: adamw_types
 };
+// The types that a table's arrays have, which a launch of others must not follow. From one on: a table of zeros has none.
+constexpr int32_t adamw_types(bool p_bf16, bool g_bf16, bool q8, bool copy) {
+  return 1 + (p_bf16 ? 1 : 0) + (g_bf16 ? 2 : 0) + (q8 ? 4 : 0) + (copy ? 8 : 0);
+}
 struct AdamwEntry {
   AdamwTensor t;
   int32_t first;     // its first chunk
