@@ -411,7 +411,8 @@ BEAM_API size_t beam_head_loss_backward_workspace_bytes(int64_t T, int64_t V, in
  *   m, v       the states, state_dtype, updated: BEAM_F32, or BEAM_FP8_E4M3: uint8 E4M3FN codes of m and of
  *              sqrt(v), each times the scale of its 256 values
  *   m_scale, v_scale  [ceil(count / 256)] fp32, updated (BEAM_FP8_E4M3 only; 4-byte aligned): a block's largest
- *              magnitude (at least 2^-100) / 448. Zero codes with any scale start a run.
+ *              magnitude (at least 2^-100) / 448. Zero codes with any finite scale start a run (an
+ *              infinite or NaN one is a block whose states are lost).
  *   copy       bf16 out: the updated FP32 weights rounded to nearest even, or NULL (for all tensors or none)
  * The call's numbers (a host struct, read before the call returns):
  *   step       t >= 1, or step_on_device: a device int32 (4-byte aligned) read by the launches instead
