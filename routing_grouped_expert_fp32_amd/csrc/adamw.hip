@@ -193,10 +193,9 @@ __device__ __forceinline__ void adamw_wave(const AdamwEntry& e, int64_t block0, 
   if (scaled) scale_bits = __float_as_int(*scale);
 
   floatx4 m_new[U], root[U];
-  uint32_t bits[U][4], most[2 * U];
+  uint32_t bits[U][4], most[2 * U] = {};   // of the blocks behind the tensor's end too
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    most[2 * u] = most[2 * u + 1] = 0;
     if (!FULL && 256 * u >= left) break;   // wave-uniform
     const int i = 256 * u + 4 * lane, n = have(u);
     floatx4 p, g, m, v;
