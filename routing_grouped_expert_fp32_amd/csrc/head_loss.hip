@@ -29,10 +29,34 @@ namespace beam {
 
 namespace {
 
-// cap tanh(z / cap), absolute error a few 2^-24 cap
-__device__ __forceinline__ float soft_cap(float z, float cap, float inv_cap) {
-  const float e = __builtin_amdgcn_exp2f(z * inv_cap * 2.885390082f);   // e^(2 z / cap)
-  return cap * (1.f - 2.f * __builtin_amdgcn_rcpf(1.f + e));
+// Capped logits cap tanh(r), r = z / cap, within 4 2^-23 of themselves, and with SLOPE their slopes 1 - tanh(r)^2. To
+// |r| = 1 tanh(r) / r is the continued fraction's (945 + 105 y + y^2) / (945 + 420 y + 15 y^2), y = r^2, off by 2^-24 there
+// and less below; past it tanh = 1 - 2 s and the slope is 4 s (1 - s), s = 1 / (1 + e^2|r|), which would cancel near zero
+// (all of 1e-4 for a logit of 1 under a cap of 1024), as 1 - tanh^2 does near the cap. Few logits of a model are past
+// its cap: the wave leaves that branch out where none is.
+template <bool SLOPE>
+__device__ __forceinline__ void soft_cap(floatx4& z, floatx4& slope, float cap, float inv_cap) {
+  floatx4 r;
+  float most = 0.f;   // a NaN stays one through the fraction
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    r[c] = z[c] * inv_cap;
+    const float y = r[c] * r[c];
+    most = fmaxf(most, y);
+    const float t = __builtin_fmaf(y, y + 105.f, 945.f) *
+                    __builtin_amdgcn_rcpf(__builtin_fmaf(y, __builtin_fmaf(y, 15.f, 420.f), 945.f));
+    const float full = z[c];
+    z[c] = full * t;
+    if constexpr (SLOPE) slope[c] = 1.f - (r[c] * t) * (r[c] * t);
+    r[c] = y <= 1.f ? 0.f : r[c];   // what is left: past 1
+  }
+  if (!__any(most > 1.f)) return;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(fabsf(r[c]) * 2.885390082f));
+    z[c] = r[c] == 0.f ? z[c] : copysignf(cap * (1.f - 2.f * s), r[c]);
+    if constexpr (SLOPE) slope[c] = r[c] == 0.f ? slope[c] : 4.f * s * (1.f - s);
+  }
 }
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.442695041f); }
 
@@ -62,34 +86,34 @@ __device__ __forceinline__ float2 logit_row(const LogitArgs& a, floatx4 (&z4)[N]
     const float lse = a.lse[t], inv = a.inv_c[t];
     const bool counts = in && inv != 0.f;   // a row without a loss may hold anything
 #pragma unroll
-    for (int j = 0; j < N; ++j)
+    for (int j = 0; j < N; ++j) {
+      floatx4 slope = {1.f, 1.f, 1.f, 1.f};
+      if constexpr (CAP) soft_cap<true>(z4[j], slope, a.cap, inv_cap);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int n = n0 + 16 * j + c;
-        float z = z4[j][c], slope = 1.f;
-        if constexpr (CAP) {
-          z = soft_cap(z, a.cap, inv_cap);
-          const float r = z * inv_cap;
-          slope = 1.f - r * r;
-        }
-        const float p = exp_fast(z - lse) - (n == y ? 1.f : 0.f);
-        z4[j][c] = n < cols && counts ? p * slope * inv : 0.f;
+        const float p = exp_fast(z4[j][c] - lse) - (n == y ? 1.f : 0.f);
+        z4[j][c] = n < cols && counts ? p * slope[c] * inv : 0.f;
       }
+      // computed here: left to the stores, behind the next caps' branches, it would take the slopes' registers along
+      if constexpr (CAP) asm volatile("" : "+v"(z4[j]));
+    }
     return make_float2(0.f, 0.f);
   } else {
     float top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < N; ++j)
+    for (int j = 0; j < N; ++j) {
+      floatx4 unused;
+      if constexpr (CAP) soft_cap<false>(z4[j], unused, a.cap, inv_cap);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int n = n0 + 16 * j + c;
-        float z = z4[j][c];
-        if constexpr (CAP) z = soft_cap(z, a.cap, inv_cap);
-        z = n < cols ? z : -INFINITY;
+        const float z = n < cols ? z4[j][c] : -INFINITY;
         z4[j][c] = z;
         top = fmaxf(top, z);
         if (in && n == y && n < cols) a.at_target[t] = z;
       }
+    }
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
     const float from = top == -INFINITY ? 0.f : top;   // no column: every term is e^-inf
@@ -292,9 +316,10 @@ __global__ __launch_bounds__(kScaleThreads) void head_scale_kernel(ScaleArgs a) 
     for (int k = 1; k < kScaleThreads / 64; ++k) z += waves[k];
     float slope = 1.f;
     if (a.cap > 0.f) {
-      z = soft_cap(z, a.cap, 1.f / a.cap);
-      const float r = z / a.cap;
-      slope = 1.f - r * r;
+      floatx4 z4 = {z, 0.f, 0.f, 0.f}, slopes;
+      soft_cap<true>(z4, slopes, a.cap, 1.f / a.cap);
+      z = z4.x;
+      slope = slopes.x;
     }
     const float share = fmaxf((1.f - exp_fast(z - a.lse[t])) * slope, 0x1p-20f);   // NaN: the floor
     c = a.d_loss[t] * share;
