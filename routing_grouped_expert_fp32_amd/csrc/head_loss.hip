@@ -10,10 +10,12 @@
 // in FP32, and over parts of a piece's contraction where its tiles are fewer than the GPU holds.
 //
 // Most of a row of dz is its target's value, whose rounding would be that of the whole row of dx and dw. So
-// dz is held as c[t] q[t][v] with c the target's value in FP32 (from a product of its own, ahead): q is -1
-// there, exactly, and under 1 beside it. dx takes c behind its sums; dw takes it in bf16(c x), whose
-// roundings are independent from value to value. (Against 64 bits, T = 1: dx 3.9e-3 at worst without, 1.7e-3
-// with it, which is the last rounding's.)
+// dz is held as c[t] q[t][v], c = d_loss max((1 - p) slope, 2^-20) of the target in FP32, from a product of its own,
+// ahead. q at the target is then -1, up to what the two products' logits differ by over 1 - p, and at most 1 beside it
+// without a cap; a target near the cap has a smaller slope than the others, whose q are up to 2^20; and where 1 - p
+// is under the floor, q is what it leaves of dz. Any of these is rounded by 2^-9 of itself, as dz itself would be. dx
+// takes c behind its sums; dw takes it in bf16(c x), whose roundings are independent from value to value. (Against 64
+// bits, T = 1: dx 3.9e-3 at worst without, 1.7e-3 with it, which is the last rounding's.)
 //
 // Bound by the matrix cores, three products of T x V x H with the loss's as a fourth (4096 tokens, 131072 x 5120: loss
 // 4.43 ms, 1240 TFLOP/s, gradient 13.2 ms, 1250); for few tokens by reading w (32 tokens: loss 200 us, 6.7 TB/s), twice
