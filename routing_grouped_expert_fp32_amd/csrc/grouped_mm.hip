@@ -17,6 +17,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "gemm_tile.h"
 #include "row_blocks.h"
 
 namespace beam {

@@ -1,10 +1,11 @@
 // Blocks of rows of the products grouped by expert, found on the device from the offsets (gfx950): shared
-// by the grouped products and the gated ones.
+// by the grouped products and the gated ones. Device code, but for the wave's exchanges plain C++: included behind the
+// header that declares those (gemm_tile.h; a check on the CPU hands in its own and runs the lanes in turn).
 #pragma once
 
 #include <type_traits>
 
-#include "gemm_tile.h"
+#include "train_rules.h"
 
 namespace beam {
 
