@@ -35,14 +35,6 @@ struct AdamwBatch {
 };
 static_assert(sizeof(AdamwBatch) + sizeof(AdamwScalars) + 16 <= 4096, "kernel arguments");
 
-__device__ __forceinline__ uint32_t mix32(uint32_t x) {
-  x ^= x >> 16;
-  x *= 0x7FEB352Du;
-  x ^= x >> 15;
-  x *= 0x846CA68Bu;
-  return x ^ (x >> 16);
-}
-
 // Pointers out of a table are to global memory (the compiler would take the slower flat accesses).
 template <class T>
 __device__ __forceinline__ __attribute__((address_space(1))) T* global_at(const void* p, int64_t i) {

@@ -65,14 +65,6 @@ beam_status_t check_head(int64_t T, int64_t V, int32_t H, float softcap) {
   return BEAM_OK;
 }
 
-uint32_t mix32(uint32_t x) {
-  x ^= x >> 16;
-  x *= 0x7FEB352Du;
-  x ^= x >> 15;
-  x *= 0x846CA68Bu;
-  return x ^ (x >> 16);
-}
-
 beam_status_t check_adamw_types(int32_t n, int32_t p, int32_t g, int32_t state) {
   if (n < 0) return BEAM_ERR_SHAPE;
   if ((p != BEAM_F32 && p != BEAM_BF16) || (g != BEAM_F32 && g != BEAM_BF16) ||
@@ -336,8 +328,8 @@ beam_status_t beam_moe_adamw(const beam_adamw_tensor* tensors, int32_t n, int32_
   s.root_scale = (float)(1.0 / std::sqrt(1.0 - std::pow(c.beta2, (double)c.step)));
   s.log_beta1 = (float)std::log(c.beta1);
   s.log_beta2 = (float)std::log(c.beta2);
-  s.key = mix32(c.seed);
-  if (!c.step_on_device) s.key = mix32(s.key + (uint32_t)c.step);
+  s.key = beam::mix32(c.seed);
+  if (!c.step_on_device) s.key = beam::mix32(s.key + (uint32_t)c.step);
   s.step = c.step_on_device;
   s.lr_now = c.lr_on_device;
   s.grad_scale = c.grad_scale;

@@ -123,6 +123,14 @@ bool head_grid_fits(int64_t T, int64_t V, int64_t H);
 struct AdamwTableHead {
   int32_t entries, chunks, types, unused;   // types: adamw_types
 };
+// The random bits of stochastic rounding: the published integer hash lowbias32 of seed, step and the value's number.
+constexpr uint32_t mix32(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x7FEB352Du;
+  x ^= x >> 15;
+  x *= 0x846CA68Bu;
+  return x ^ (x >> 16);
+}
 // The types that a table's arrays have, which a launch of others must not follow. From one on: a table of zeros has none.
 constexpr int32_t adamw_types(bool p_bf16, bool g_bf16, bool q8, bool copy) {
   return 1 + (p_bf16 ? 1 : 0) + (g_bf16 ? 2 : 0) + (q8 ? 4 : 0) + (copy ? 8 : 0);
