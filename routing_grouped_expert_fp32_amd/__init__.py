@@ -188,12 +188,6 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
-
-
 def workspace_bytes(cfg: Cfg, T: int) -> int:
     return int(lib().beam_moe_workspace_bytes(ctypes.byref(cfg), T))
 
@@ -202,26 +196,20 @@ def route_workspace_bytes(cfg: Cfg, T: int) -> int:
     return int(lib().beam_moe_route_workspace_bytes(ctypes.byref(cfg), T))
 
 
-def _check_dev(*ts):
-    for t in ts:
-        if t is not None and (not t.is_cuda or not t.is_contiguous()):
-            raise ValueError("tensors must be contiguous device tensors")
-
-
 def route(x, w_router, bias, cfg: Cfg, topk_ids=None, topk_w=None, workspace=None, stream=None):
     """beam_moe_route: returns (topk_ids int32 [T][K], topk_w fp32 [T][K])."""
     T = x.shape[0]
-    if topk_ids is None:
-        topk_ids = torch.empty((T, cfg.topk), dtype=torch.int32, device=x.device)
-    if topk_w is None:
-        topk_w = torch.empty((T, cfg.topk), dtype=torch.float32, device=x.device)
-    nbytes = route_workspace_bytes(cfg, T)
-    if workspace is None:
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
-    _check_dev(x, w_router, bias, topk_ids, topk_w, workspace)
-    rc = lib().beam_moe_route(_ptr(x), _ptr(w_router), _ptr(bias), _ptr(topk_ids), _ptr(topk_w),
-                              T, ctypes.byref(cfg), _ptr(workspace), workspace.numel(),
-                              _stream(stream))
+    ctx, st = _on(_device_of(x, w_router, bias, topk_ids, topk_w, workspace), stream)
+    with ctx:
+        if topk_ids is None:
+            topk_ids = torch.empty((T, cfg.topk), dtype=torch.int32, device=x.device)
+        if topk_w is None:
+            topk_w = torch.empty((T, cfg.topk), dtype=torch.float32, device=x.device)
+        nbytes = route_workspace_bytes(cfg, T)
+        if workspace is None:
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
+        rc = lib().beam_moe_route(_ptr(x), _ptr(w_router), _ptr(bias), _ptr(topk_ids), _ptr(topk_w),
+                                  T, ctypes.byref(cfg), _ptr(workspace), workspace.numel(), st)
     if rc != 0:
         raise BeamError(rc, "beam_moe_route")
     return topk_ids, topk_w
@@ -231,19 +219,19 @@ def forward(x, w_router, bias, w_gate_up, w_down, cfg: Cfg, out=None, w_gate_up_
             w_down_scale=None, topk_ids_out=None, topk_w_out=None, workspace=None, stream=None):
     """beam_moe_forward: returns out [T][H] (fp32 unless cfg.out_dtype is bf16)."""
     T = x.shape[0]
-    if out is None:
-        odt = torch.bfloat16 if cfg.out_dtype == BEAM_BF16 else torch.float32
-        out = torch.empty((T, cfg.hidden), dtype=odt, device=x.device)
-    nbytes = workspace_bytes(cfg, T)
-    if workspace is None:
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
-    _check_dev(x, w_router, bias, w_gate_up, w_down, out, w_gate_up_scale, w_down_scale,
-               topk_ids_out, topk_w_out, workspace)
-    rc = lib().beam_moe_forward(_ptr(x), _ptr(w_router), _ptr(bias), _ptr(w_gate_up),
-                                _ptr(w_down), _ptr(out), T, ctypes.byref(cfg),
-                                _ptr(w_gate_up_scale), _ptr(w_down_scale), _ptr(topk_ids_out),
-                                _ptr(topk_w_out), _ptr(workspace), workspace.numel(),
-                                _stream(stream))
+    ctx, st = _on(_device_of(x, w_router, bias, w_gate_up, w_down, out, w_gate_up_scale,
+                             w_down_scale, topk_ids_out, topk_w_out, workspace), stream)
+    with ctx:
+        if out is None:
+            odt = torch.bfloat16 if cfg.out_dtype == BEAM_BF16 else torch.float32
+            out = torch.empty((T, cfg.hidden), dtype=odt, device=x.device)
+        nbytes = workspace_bytes(cfg, T)
+        if workspace is None:
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
+        rc = lib().beam_moe_forward(_ptr(x), _ptr(w_router), _ptr(bias), _ptr(w_gate_up),
+                                    _ptr(w_down), _ptr(out), T, ctypes.byref(cfg),
+                                    _ptr(w_gate_up_scale), _ptr(w_down_scale), _ptr(topk_ids_out),
+                                    _ptr(topk_w_out), _ptr(workspace), workspace.numel(), st)
     if rc != 0:
         raise BeamError(rc, "beam_moe_forward")
     return out
@@ -253,15 +241,16 @@ def forward_noalloc(x, w_router, bias, w_gate_up, w_down, cfg: Cfg, out=None, w_
                     w_down_scale=None, topk_ids_out=None, topk_w_out=None, stream=None):
     """beam_moe_forward_noalloc: beam_moe_forward on the library's own per-GPU workspace."""
     T = x.shape[0]
-    if out is None:
-        odt = torch.bfloat16 if cfg.out_dtype == BEAM_BF16 else torch.float32
-        out = torch.empty((T, cfg.hidden), dtype=odt, device=x.device)
-    _check_dev(x, w_router, bias, w_gate_up, w_down, out, w_gate_up_scale, w_down_scale,
-               topk_ids_out, topk_w_out)
-    rc = lib().beam_moe_forward_noalloc(_ptr(x), _ptr(w_router), _ptr(bias), _ptr(w_gate_up),
-                                        _ptr(w_down), _ptr(out), T, ctypes.byref(cfg),
-                                        _ptr(w_gate_up_scale), _ptr(w_down_scale),
-                                        _ptr(topk_ids_out), _ptr(topk_w_out), _stream(stream))
+    ctx, st = _on(_device_of(x, w_router, bias, w_gate_up, w_down, out, w_gate_up_scale,
+                             w_down_scale, topk_ids_out, topk_w_out), stream)
+    with ctx:
+        if out is None:
+            odt = torch.bfloat16 if cfg.out_dtype == BEAM_BF16 else torch.float32
+            out = torch.empty((T, cfg.hidden), dtype=odt, device=x.device)
+        rc = lib().beam_moe_forward_noalloc(_ptr(x), _ptr(w_router), _ptr(bias), _ptr(w_gate_up),
+                                            _ptr(w_down), _ptr(out), T, ctypes.byref(cfg),
+                                            _ptr(w_gate_up_scale), _ptr(w_down_scale),
+                                            _ptr(topk_ids_out), _ptr(topk_w_out), st)
     if rc != 0:
         raise BeamError(rc, "beam_moe_forward_noalloc")
     return out
@@ -275,19 +264,19 @@ def forward_routed(x, topk_ids, topk_w, w_gate_up, w_down, cfg: Cfg, expert_begi
     T = x.shape[0]
     if expert_end is None:
         expert_end = cfg.n_experts
-    if out is None:
-        odt = torch.bfloat16 if cfg.out_dtype == BEAM_BF16 else torch.float32
-        out = torch.empty((T, cfg.hidden), dtype=odt, device=x.device)
-    nbytes = workspace_bytes(cfg, T)
-    if workspace is None:
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
-    _check_dev(x, topk_ids, topk_w, w_gate_up, w_down, out, w_gate_up_scale, w_down_scale,
-               workspace)
-    rc = lib().beam_moe_forward_routed(_ptr(x), _ptr(topk_ids), _ptr(topk_w), _ptr(w_gate_up),
-                                       _ptr(w_down), _ptr(out), T, ctypes.byref(cfg),
-                                       int(expert_begin), int(expert_end), _ptr(w_gate_up_scale),
-                                       _ptr(w_down_scale), _ptr(workspace), workspace.numel(),
-                                       _stream(stream))
+    ctx, st = _on(_device_of(x, topk_ids, topk_w, w_gate_up, w_down, out, w_gate_up_scale,
+                             w_down_scale, workspace), stream)
+    with ctx:
+        if out is None:
+            odt = torch.bfloat16 if cfg.out_dtype == BEAM_BF16 else torch.float32
+            out = torch.empty((T, cfg.hidden), dtype=odt, device=x.device)
+        nbytes = workspace_bytes(cfg, T)
+        if workspace is None:
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
+        rc = lib().beam_moe_forward_routed(_ptr(x), _ptr(topk_ids), _ptr(topk_w), _ptr(w_gate_up),
+                                           _ptr(w_down), _ptr(out), T, ctypes.byref(cfg),
+                                           int(expert_begin), int(expert_end), _ptr(w_gate_up_scale),
+                                           _ptr(w_down_scale), _ptr(workspace), workspace.numel(), st)
     if rc != 0:
         raise BeamError(rc, "beam_moe_forward_routed")
     return out
@@ -303,16 +292,17 @@ def dense_mlp(x, w_gate_up, w_down, out=None, out_dtype=BEAM_F32, w_gate_up_scal
     T, H = x.shape
     F = w_gate_up.shape[0] // 2
     wdt = _DT_CODE[w_gate_up.dtype]
-    if out is None:
-        odt = torch.bfloat16 if out_dtype == BEAM_BF16 else torch.float32
-        out = torch.empty((T, H), dtype=odt, device=x.device)
-    if workspace is None:
-        workspace = torch.empty(max(dense_workspace_bytes(H, F, wdt, T), 16), dtype=torch.uint8,
-                                device=x.device)
-    _check_dev(x, w_gate_up, w_down, out, w_gate_up_scale, w_down_scale, workspace)
-    rc = lib().beam_dense_mlp_forward(_ptr(x), _ptr(w_gate_up), _ptr(w_down), _ptr(out), T, H, F,
-                                      wdt, out_dtype, _ptr(w_gate_up_scale), _ptr(w_down_scale),
-                                      _ptr(workspace), workspace.numel(), _stream(stream))
+    ctx, st = _on(_device_of(x, w_gate_up, w_down, out, w_gate_up_scale, w_down_scale, workspace), stream)
+    with ctx:
+        if out is None:
+            odt = torch.bfloat16 if out_dtype == BEAM_BF16 else torch.float32
+            out = torch.empty((T, H), dtype=odt, device=x.device)
+        if workspace is None:
+            workspace = torch.empty(max(dense_workspace_bytes(H, F, wdt, T), 16), dtype=torch.uint8,
+                                    device=x.device)
+        rc = lib().beam_dense_mlp_forward(_ptr(x), _ptr(w_gate_up), _ptr(w_down), _ptr(out), T, H, F,
+                                          wdt, out_dtype, _ptr(w_gate_up_scale), _ptr(w_down_scale),
+                                          _ptr(workspace), workspace.numel(), st)
     if rc != 0:
         raise BeamError(rc, "beam_dense_mlp_forward")
     return out
@@ -322,14 +312,15 @@ def residual_boundary(y, h, gamma_post, gamma_next, depth_n: int, eps: float, h_
                       x_next=None, stream=None):
     """beam_residual_boundary: returns (h_out, x_next), both bf16 [T][hidden]."""
     T, H = h.shape
-    if h_out is None:
-        h_out = torch.empty_like(h)
-    if x_next is None:
-        x_next = torch.empty_like(h)
-    _check_dev(y, h, gamma_post, gamma_next, h_out, x_next)
-    rc = lib().beam_residual_boundary(_ptr(y), _DT_CODE[y.dtype], _ptr(h), _ptr(gamma_post),
-                                      _ptr(gamma_next), _ptr(h_out), _ptr(x_next), T, H,
-                                      int(depth_n), float(eps), _stream(stream))
+    ctx, st = _on(_device_of(y, h, gamma_post, gamma_next, h_out, x_next), stream)
+    with ctx:
+        if h_out is None:
+            h_out = torch.empty_like(h)
+        if x_next is None:
+            x_next = torch.empty_like(h)
+        rc = lib().beam_residual_boundary(_ptr(y), _DT_CODE[y.dtype], _ptr(h), _ptr(gamma_post),
+                                          _ptr(gamma_next), _ptr(h_out), _ptr(x_next), T, H,
+                                          int(depth_n), float(eps), st)
     if rc != 0:
         raise BeamError(rc, "beam_residual_boundary")
     return h_out, x_next
@@ -342,20 +333,22 @@ def forward_boundary(x, w_router, bias, w_gate_up, w_down, cfg: Cfg, h, gamma_po
     """beam_moe_forward_boundary: the MoE block with its combine fused into the following
     norm -> residual -> norm boundary; returns (h_out, x_next)."""
     T = x.shape[0]
-    if h_out is None:
-        h_out = torch.empty_like(h)
-    if x_next is None:
-        x_next = torch.empty_like(h)
-    nbytes = workspace_bytes(cfg, T)
-    if workspace is None:
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
-    _check_dev(x, w_router, bias, w_gate_up, w_down, h, gamma_post, gamma_next, h_out, x_next,
-               w_gate_up_scale, w_down_scale, topk_ids_out, topk_w_out, workspace)
-    rc = lib().beam_moe_forward_boundary(
-        _ptr(x), _ptr(w_router), _ptr(bias), _ptr(w_gate_up), _ptr(w_down), T, ctypes.byref(cfg),
-        _ptr(w_gate_up_scale), _ptr(w_down_scale), _ptr(h), _ptr(gamma_post), _ptr(gamma_next),
-        int(depth_n), float(eps), _ptr(h_out), _ptr(x_next), _ptr(topk_ids_out), _ptr(topk_w_out),
-        _ptr(workspace), workspace.numel(), _stream(stream))
+    ctx, st = _on(_device_of(x, w_router, bias, w_gate_up, w_down, h, gamma_post, gamma_next,
+                             h_out, x_next, w_gate_up_scale, w_down_scale, topk_ids_out,
+                             topk_w_out, workspace), stream)
+    with ctx:
+        if h_out is None:
+            h_out = torch.empty_like(h)
+        if x_next is None:
+            x_next = torch.empty_like(h)
+        nbytes = workspace_bytes(cfg, T)
+        if workspace is None:
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
+        rc = lib().beam_moe_forward_boundary(
+            _ptr(x), _ptr(w_router), _ptr(bias), _ptr(w_gate_up), _ptr(w_down), T, ctypes.byref(cfg),
+            _ptr(w_gate_up_scale), _ptr(w_down_scale), _ptr(h), _ptr(gamma_post), _ptr(gamma_next),
+            int(depth_n), float(eps), _ptr(h_out), _ptr(x_next), _ptr(topk_ids_out), _ptr(topk_w_out),
+            _ptr(workspace), workspace.numel(), st)
     if rc != 0:
         raise BeamError(rc, "beam_moe_forward_boundary")
     return h_out, x_next
@@ -364,13 +357,13 @@ def forward_boundary(x, w_router, bias, w_gate_up, w_down, cfg: Cfg, h, gamma_po
 def quant_fp8(src, codes=None, scales=None, stream=None):
     """beam_moe_quant_fp8 on bf16 rows src [rows][cols]: returns (codes uint8, scales fp32)."""
     rows, cols = src.shape
-    if codes is None:
-        codes = torch.empty((rows, cols), dtype=torch.uint8, device=src.device)
-    if scales is None:
-        scales = torch.empty((rows,), dtype=torch.float32, device=src.device)
-    _check_dev(src, codes, scales)
-    rc = lib().beam_moe_quant_fp8(_ptr(src), rows, cols, _ptr(codes), _ptr(scales),
-                                  _stream(stream))
+    ctx, st = _on(_device_of(src, codes, scales), stream)
+    with ctx:
+        if codes is None:
+            codes = torch.empty((rows, cols), dtype=torch.uint8, device=src.device)
+        if scales is None:
+            scales = torch.empty((rows,), dtype=torch.float32, device=src.device)
+        rc = lib().beam_moe_quant_fp8(_ptr(src), rows, cols, _ptr(codes), _ptr(scales), st)
     if rc != 0:
         raise BeamError(rc, "beam_moe_quant_fp8")
     return codes, scales
@@ -380,11 +373,12 @@ def convert(src, dst_dtype: int, dst=None, stream=None):
     """beam_moe_convert: fp32 [n] -> bf16 (BEAM_BF16, returned as torch.bfloat16) or E4M3 codes
     (BEAM_FP8_E4M3, returned as uint8) with the kernels' rounding routines."""
     n = src.numel()
-    if dst is None:
-        dt = torch.bfloat16 if dst_dtype == BEAM_BF16 else torch.uint8
-        dst = torch.empty(src.shape, dtype=dt, device=src.device)
-    _check_dev(src, dst)
-    rc = lib().beam_moe_convert(_ptr(src), n, dst_dtype, _ptr(dst), _stream(stream))
+    ctx, st = _on(_device_of(src, dst), stream)
+    with ctx:
+        if dst is None:
+            dt = torch.bfloat16 if dst_dtype == BEAM_BF16 else torch.uint8
+            dst = torch.empty(src.shape, dtype=dt, device=src.device)
+        rc = lib().beam_moe_convert(_ptr(src), n, dst_dtype, _ptr(dst), st)
     if rc != 0:
         raise BeamError(rc, "beam_moe_convert")
     return dst
@@ -392,10 +386,10 @@ def convert(src, dst_dtype: int, dst=None, stream=None):
 
 def fp8_dot_tiles(a, b, c, stream=None):
     """beam_moe_fp8_dot_tiles on uint8 codes a, b [n][16][128] and fp32 c [n][16][16]: returns d."""
-    d = torch.empty_like(c)
-    _check_dev(a, b, c, d)
-    rc = lib().beam_moe_fp8_dot_tiles(_ptr(a), _ptr(b), _ptr(c), _ptr(d), a.shape[0],
-                                      _stream(stream))
+    ctx, st = _on(_device_of(a, b, c), stream)
+    with ctx:
+        d = torch.empty_like(c)
+        rc = lib().beam_moe_fp8_dot_tiles(_ptr(a), _ptr(b), _ptr(c), _ptr(d), a.shape[0], st)
     if rc != 0:
         raise BeamError(rc, "beam_moe_fp8_dot_tiles")
     return d
@@ -421,13 +415,14 @@ def _on(dev, stream):
     """(context, stream handle): the context makes the tensors' device and the stream (default: its
     current one) current, so that results and workspaces allocated inside belong to the stream that
     uses them."""
-    if stream is None:
-        # torch.cuda.current_stream(dev).cuda_stream without the Stream object, 1.8 us of a call's 10
-        handle = torch._C._cuda_getCurrentRawStream(dev)
-        return (_NO_CONTEXT if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)), handle
-    if stream.device.index != dev:
-        raise ValueError("the stream is on another device than the tensors")
-    return torch.cuda.stream(stream), stream.cuda_stream
+    # torch.cuda.current_stream(dev).cuda_stream without the Stream object, 1.8 us of a call's 10
+    handle = torch._C._cuda_getCurrentRawStream(dev)
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError("the stream is on another device than the tensors")
+        if stream.cuda_stream != handle:   # (a context that changes nothing would cost 4 us)
+            return torch.cuda.stream(stream), stream.cuda_stream
+    return (_NO_CONTEXT if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)), handle
 
 
 class _NoContext:
