@@ -35,30 +35,37 @@ namespace {
 // |r| = 1 tanh(r) / r is the continued fraction's (945 + 105 y + y^2) / (945 + 420 y + 15 y^2), y = r^2, off by 2^-24 there
 // and less below; past it tanh = 1 - 2 s and the slope is 4 s (1 - s), s = 1 / (1 + e^2|r|), which would cancel near zero
 // (all of 1e-4 for a logit of 1 under a cap of 1024), as 1 - tanh^2 does near the cap. Few logits of a model are past
-// its cap: the wave leaves that branch out where none is.
+// its cap: a wave whose row has none (`past`) leaves that out.
 template <bool SLOPE>
-__device__ __forceinline__ void soft_cap(floatx4& z, floatx4& slope, float cap, float inv_cap) {
+__device__ __forceinline__ void soft_cap(floatx4& z, floatx4& slope, float cap, float inv_cap, bool past) {
   floatx4 r;
-  float most = 0.f;   // a NaN stays one through the fraction
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     r[c] = z[c] * inv_cap;
     const float y = r[c] * r[c];
-    most = fmaxf(most, y);
     const float t = __builtin_fmaf(y, y + 105.f, 945.f) *
                     __builtin_amdgcn_rcpf(__builtin_fmaf(y, __builtin_fmaf(y, 15.f, 420.f), 945.f));
-    const float full = z[c];
-    z[c] = full * t;
+    z[c] *= t;
     if constexpr (SLOPE) slope[c] = 1.f - (r[c] * t) * (r[c] * t);
-    r[c] = y <= 1.f ? 0.f : r[c];   // what is left: past 1
   }
-  if (!__any(most > 1.f)) return;
+  if (!past) return;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(fabsf(r[c]) * 2.885390082f));
-    z[c] = r[c] == 0.f ? z[c] : copysignf(cap * (1.f - 2.f * s), r[c]);
-    if constexpr (SLOPE) slope[c] = r[c] == 0.f ? slope[c] : 4.f * s * (1.f - s);
+    const bool within = r[c] * r[c] <= 1.f;
+    z[c] = within ? z[c] : copysignf(cap * (1.f - 2.f * s), r[c]);
+    if constexpr (SLOPE) slope[c] = within ? slope[c] : 4.f * s * (1.f - s);
   }
+}
+// Whether the wave has a logit past the cap (r^2 > 1 implies it; a NaN stays one through the fraction).
+template <int N>
+__device__ __forceinline__ bool any_past(const floatx4 (&z4)[N], float cap) {
+  float most = 0.f;
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) most = fmaxf(most, fabsf(z4[j][c]));
+  return __any(most > 0.999999f * cap);
 }
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.442695041f); }
 
@@ -82,6 +89,7 @@ template <bool GRAD, bool CAP, int N>
 __device__ __forceinline__ float2 logit_row(const LogitArgs& a, floatx4 (&z4)[N], int row0, int m, bool in, int col0,
                                             int n0, int cols) {
   const float inv_cap = CAP ? 1.f / a.cap : 0.f;
+  const bool past = CAP && any_past(z4, a.cap);
   const int t = row0 + (in ? m : 0);
   const int y = a.targets[t] - a.v0 - col0;   // the target's column of this tile, if it has one
   if constexpr (GRAD) {
@@ -90,7 +98,7 @@ __device__ __forceinline__ float2 logit_row(const LogitArgs& a, floatx4 (&z4)[N]
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       floatx4 slope = {1.f, 1.f, 1.f, 1.f};
-      if constexpr (CAP) soft_cap<true>(z4[j], slope, a.cap, inv_cap);
+      if constexpr (CAP) soft_cap<true>(z4[j], slope, a.cap, inv_cap, past);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int n = n0 + 16 * j + c;
@@ -106,7 +114,7 @@ __device__ __forceinline__ float2 logit_row(const LogitArgs& a, floatx4 (&z4)[N]
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       floatx4 unused;
-      if constexpr (CAP) soft_cap<false>(z4[j], unused, a.cap, inv_cap);
+      if constexpr (CAP) soft_cap<false>(z4[j], unused, a.cap, inv_cap, past);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int n = n0 + 16 * j + c;
@@ -318,9 +326,9 @@ __global__ __launch_bounds__(kScaleThreads) void head_scale_kernel(ScaleArgs a) 
     for (int k = 1; k < kScaleThreads / 64; ++k) z += waves[k];
     float slope = 1.f;
     if (a.cap > 0.f) {
-      floatx4 z4 = {z, 0.f, 0.f, 0.f}, slopes;
-      soft_cap<true>(z4, slopes, a.cap, 1.f / a.cap);
-      z = z4.x;
+      floatx4 z4[1] = {{z, 0.f, 0.f, 0.f}}, slopes;
+      soft_cap<true>(z4[0], slopes, a.cap, 1.f / a.cap, any_past(z4, a.cap));
+      z = z4[0].x;
       slope = slopes.x;
     }
     const float share = fmaxf((1.f - exp_fast(z - a.lse[t])) * slope, 0x1p-20f);   // NaN: the floor
