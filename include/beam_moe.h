@@ -386,9 +386,10 @@ BEAM_API size_t beam_moe_gated_mm_backward_workspace_bytes(int64_t R, int32_t F)
  *   workspace  at least beam_head_loss_workspace_bytes, beam_head_loss_backward_workspace_bytes(T, V, H)
  * Logits are FP32 sums of exact products; e^z, their sums and dz are FP32. dz is rounded to bf16 for the two
  * products, whose sums are FP32 again: dx and dw carry that rounding (2^-9 of each of their terms), an FP32 dw
- * too. The gradient works on pieces of the vocabulary: 512 MiB of dz at a time, or 32768 columns up to 4 GiB; the
- * loss keeps 8 bytes for each token and 64 to 256 columns. T = 0: no-ops, but dw is set to zero (the other
- * pointers may then be NULL). Equal calls give equal bits.
+ * too. The cap and its slope are within a few 2^-23 of themselves. The gradient works on pieces of the vocabulary:
+ * 512 MiB of dz at a time, or 32768 columns up to 4 GiB, or, of more than 2^22 tokens, 512 columns (16 GiB for 2^24
+ * tokens); the loss keeps 8 bytes for each token and 32 to 256 columns. T = 0: no-ops, but dw is set to zero (the
+ * other pointers may then be NULL). Equal calls give equal bits.
  * Limits: H % 8 == 0, H <= 2^20, V <= 2^23, T < 2^24, and launches of fewer than 2^32 threads. */
 BEAM_API beam_status_t beam_head_loss(const void* x, const void* w, const int32_t* targets, float* loss,
                                       float* lse, int64_t T, int64_t V, int32_t H, float softcap,

@@ -13,16 +13,17 @@
 // nearest (half a step of E4M3 is 3 to 6%). A root above zero stays above zero, else the next update of a
 // value far below its block's largest would be divided by eps.
 //
-// Bound by memory: 28 bytes a value (FP32 weights and states, bf16 gradients and copies: 4e8 values in 2.01 ms,
-// 5.6 TB/s), 10 with 8-bit states and bf16 weights (0.78 ms, 5.2 TB/s, where the arithmetic of the roundings, some
-// 85 instructions a value, is near it). A wave takes kAdamwUnroll blocks of 256 values, all of its loads issued
-// ahead and non-temporal, as its stores (2.12 ms with the default policy); a lane has four consecutive values of
-// a block. The eight maxima of a wave's blocks are reduced together, each step halving what a lane holds, and
-// their eight reciprocals and eight scales are one division, a lane each (1.10 ms with a reduction and four
-// divisions a block, and codes rounded by floor and the conversion).
+// Bound by memory: 28 bytes a value (FP32 weights and states, bf16 gradients and copies: 4e8 values in 1.98 to 2.03 ms,
+// 5.6 TB/s), 10 with 8-bit states and bf16 weights (0.78 to 0.82 ms, 5.0 TB/s, where the arithmetic of the roundings,
+// some 85 instructions a value, is near it). A wave takes kAdamwUnroll blocks of 256 values, all of its loads issued
+// ahead and non-temporal, as its stores (2.12 ms with the default policy); a lane has four consecutive values of a
+// block. The eight maxima of a wave's blocks are reduced together, each step halving what a lane holds, and their eight
+// reciprocals and eight scales are one division, a lane each (1.10 ms with a reduction and four divisions a block, and
+// codes rounded by floor and the conversion).
 //
-// A workgroup finds its tensor in a table that the caller keeps on the device (one launch for a whole list: 208
-// tensors of 5120 values 8.4 us), or, without one, in the kernel's arguments, kAdamwTensors a launch (24 us).
+// A workgroup finds its tensor in a table that the caller keeps on the device (one launch for a whole list: 208 tensors
+// of 5120 values 8.3 to 8.8 us), or, without one, in the kernel's arguments, kAdamwTensors a launch (24 us; with other
+// gradients a call the checks of 208 tensors in Python take 118).
 #include "device_common.h"
 #include "step_rules.h"
 

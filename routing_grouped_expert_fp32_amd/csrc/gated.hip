@@ -15,11 +15,11 @@
 // up rows, in turns of 16, so that a wave holds g and u of the same values. Gradient: the products dh
 // never leave the registers; g and u are read, and d_g, d_u and h written, by its epilogue.
 //
-// Bound by reading the weights for few rows (32 rows, 21 of 32 experts, 5120 -> 2560: 171 us, 6.4 TB/s), by the
-// matrix cores for many (4096 rows of one expert, 5120 -> 20480: 1.39 ms, 1230 TFLOP/s), in between by the weights'
-// latency (8192 rows of 32 experts: 0.47 ms, 4.1 TB/s). The gradient's epilogue moves 10 bytes a value, which little of
-// another tile's arithmetic hides: 32768 skewed rows, 5120 -> 2560, 0.86 ms (matrix cores busy 49%). Fetching its g and
-// u ahead of the products, or two to five sub-tiles ahead, gained nothing.
+// Bound by reading the weights for few rows (32 rows, 21 of 32 experts, 5120 -> 2560: 171 us, 6.4 TB/s), by the matrix
+// cores for many (4096 rows of one expert, 5120 -> 20480: 1.38 to 1.44 ms, 1190 to 1240 TFLOP/s), in between by the
+// weights' latency (8192 rows of 32 experts: 0.46 to 0.48 ms, 4.0 TB/s). The gradient's epilogue moves 10 bytes a
+// value, which little of another tile's arithmetic hides: 32768 skewed rows, 5120 -> 2560, 0.86 to 0.88 ms (matrix
+// cores busy 49%). Fetching its g and u ahead of the products, or two to five sub-tiles ahead, gained nothing.
 #include <type_traits>
 
 #include "narrow.h"

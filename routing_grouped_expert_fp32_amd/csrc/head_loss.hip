@@ -18,8 +18,8 @@
 // bits, T = 1: dx 3.9e-3 at worst without, 1.7e-3 with it, which is the last rounding's.)
 //
 // Bound by the matrix cores, three products of T x V x H with the loss's as a fourth (4096 tokens, 131072 x 5120: loss
-// 4.43 ms, 1240 TFLOP/s, gradient 13.2 ms, 1250); for few tokens by reading w (32 tokens: loss 200 us, 6.7 TB/s), twice
-// for the gradient, and writing dw.
+// 4.4 to 4.75 ms, 1160 to 1245 TFLOP/s with the machine's clock, gradient 13.1 to 13.85, 1190 to 1260); for few tokens
+// by reading w (32 tokens: loss 200 us, 6.7 TB/s), twice for the gradient, and writing dw.
 #include <cmath>
 #include <type_traits>
 

@@ -1,9 +1,9 @@
 // Products of few rows (gfx950): a workgroup's eight waves split the contraction of one block of up to 32 rows by two
 // runs of 16 weight rows, and their sums meet in LDS. Where the tiles of gemm_tile.h are fewer than the CUs, their
-// chain of stages is what such a call takes; here a wave has an eighth of it, in kNarrowAhead turns at once.
-// Bound by reading the weights with few bytes in flight: one row, 5120 -> 2560 of the gated products, 52 MB in 13.6 us
-// (3.9 TB/s, tiles 30); rows' fragments are read again by each workgroup, so blocks of 32 rows end where tiles begin
-// to fill the CUs.
+// chain of stages is what such a call takes; here a wave has an eighth of it, in kNarrowAhead turns at once. Bound by
+// reading the weights with few bytes in flight: one row, 5120 -> 2560 of the gated products, 52 MB in 17.4 us out of
+// memory (3.0 TB/s, tiles 32), in 13.7 out of the last-level cache (tiles 29); rows' fragments are read again by each
+// workgroup, so blocks of 32 rows end where tiles begin to fill the CUs.
 #pragma once
 
 #include "gemm_tile.h"

@@ -24,11 +24,13 @@ void with_gated_tile(int64_t R, int64_t E, int64_t Fw, int64_t K, bool keep, F&&
 
 // Few rows of few experts make few tiles, each a chain of stages: blocks of 32 rows by kNarrowCols hidden values instead,
 // the contraction split over a workgroup's waves, where those are at most one and a half a CU and the chain is long.
-// Measured (us, the tiles first): one row, 5120 -> 2560, 160 blocks, 30.3, 13.6; 8 rows, 4624 -> 944, 59: 22.5, 10.8; 4
-// rows, 4096 -> 4096, 256: 25.8, 14.7; one row each of 4 experts, 5120 -> 2560, 320 to 480: 32.2, 26.5; 16 rows, 4096 ->
-// 8192, 512: 29.5, 29.9; 20 rows of 16 experts, 2048 -> 704, 528: 15.9, 21.5; 128 rows, 4096 -> 1024, 256: 23.9, 19.5; 16
-// rows, 2048 -> 1024, 64: 11.5, 8.7; 30 rows, 1024 -> 2560, 160: 8.1, 8.2. Turns of a wave at once: five; with eight
-// these are 15.7, 12.8 and 13.4 (fewer of them past the end of most contractions).
+// Measured (us, the tiles first, on weights out of memory, then on weights that the last call left in the cache): one
+// row, 5120 -> 2560, 160 blocks, 31.8, 17.4, then 29.4, 13.7; 8 rows, 4624 -> 944, 59: 29.9, 16.5, 22.2, 10.7; 4 rows, 4096
+// -> 4096, 256: 27.5, 17.6, 25.8, 15.3; one row or so of each of 4 experts, 5120 -> 2560, 320 to 640: 33.5, 35.3, 32.2,
+// 28.1; 16 rows, 4096 -> 8192, 512: 32.2, 37.3, 29.7, 31.7; 20 rows of 16 experts, 2048 -> 704, 528: 18.1, 24.4, 15.6, 22.0;
+// 128 rows, 4096 -> 1024, 256: 26.7, 21.2, 22.7, 19.5; 16 rows, 2048 -> 1024, 64: 14.1, 9.7, 11.5, 8.7; 30 rows, 1024 ->
+// 2560, 160: 9.1, 9.6, 7.7, 8.2. Turns of a wave at once: five; with eight the first three are, in the cache, 15.7, 12.8
+// and 13.4 (fewer of them past the end of most contractions).
 constexpr int kNarrowWaves = 8, kNarrowAhead = 5, kNarrowCols = 16;
 bool gated_is_narrow(int64_t R, int64_t E, int64_t Fw, int64_t K);
 
@@ -62,11 +64,12 @@ void with_head_tile(int64_t T, int64_t V, int64_t H, bool store, F&& f) {
 }
 // Few tokens and columns (`end` of them, to the pitch for the gradient): blocks of 32 tokens by kNarrowLogits columns
 // as for the gated products, where they are at most one a CU. Measured (us, the loss's logits, then the gradient's, the
-// tiles first): one token, 1000 x 1280, 32 blocks, 8.7, 6.2 and 7.0, 5.6; 2, 300 x 5120, 10: 30.2, 12.6 and 20.9, 12.3;
-// 8, 4096 x 4096, 128: 25.0, 12.7 and 17.3, 13.9; 32 of them 25.2, 17.9 and 17.4, 18.6; 16, 8192 x 5120, 256: 32.7, 18.3
-// and 21.7, 18.3; 32, 8000 x 1600, 250: 12.2, 9.6 and 8.9, 9.9; 128, 2048 x 4096, 256: 24.2, 18.5 and 21.4, 18.4. 384
-// blocks: one, 12288 x 5120 33.8, 26.5 and 22.2, 26.2; 32, 12288 x 2048 15.5, 20.3 and 10.9, 20.6; 64, 6144 x 5120 34.6,
-// 41.6 and 27.0, 41.5.
+// tiles first, on weights out of memory): one token, 1000 x 1280, 32 blocks, 9.8, 7.1 and 9.6, 6.6; 2, 300 x 5120, 10:
+// 29.7, 15.8 and 30.4, 16.0; 8, 4096 x 4096, 128: 26.2, 15.7 and 25.3, 15.9; 32 of them 26.3, 21.6 and 25.4, 21.8; 16, 8192
+// x 5120, 256: 33.7, 23.9 and 32.7, 24.3; 32, 8000 x 1600, 250: 12.8, 11.7 and 12.0, 11.5; 128, 2048 x 4096, 256: 27.9, 20.6
+// and 26.2, 20.4. 384 blocks: one, 12288 x 5120 35.2, 34.1 and 38.8, 39.7; 32, 12288 x 2048 16.4, 24.0 and 15.7, 23.4; 64,
+// 6144 x 5120 35.9, 45.0 and 33.8, 46.3. On weights that the last call left in the cache the tiles gain more: the
+// gradient's are ahead of two of these blocks (32 tokens: 17.7, 18.7 and 9.1, 10.0), the loss's of none.
 constexpr int kNarrowLogits = 32;
 inline bool head_is_narrow(int64_t T, int64_t end, int64_t H) {
   return H >= 1280 && ceil_div(T, 32) * ceil_div(end, kNarrowLogits) <= kGroupedCus;
@@ -110,8 +113,8 @@ struct HeadBwdLayout {
   bool direct() const { return pieces == 1 && dx.parts == 1; }
 };
 // Columns of a piece: what 512 MiB of dz hold, but 32768 where 4 GiB do (each piece reads and writes T x H sums of dx,
-// 8 bytes against 2 columns' products: 3% of a piece of 32768), and never under 512. 4096 tokens, 131072 x 5120, in
-// pieces of 256 MiB, 512 MiB, 1 GiB: 13.5, 13.3, 13.25 ms.
+// 8 bytes against 2 columns' products: 3% of a piece of 32768), and never under 512 (16 GiB of 2^24 tokens). 4096
+// tokens, 131072 x 5120, in pieces of 256 MiB, 512 MiB, 1 GiB: 13.5, 13.3, 13.25 ms.
 constexpr int64_t kHeadPieceBytes = int64_t(512) << 20, kHeadMostBytes = int64_t(4) << 30;
 constexpr int64_t kHeadPieceCols = 32768, kHeadLeastCols = 512;
 HeadBwdLayout head_bwd_layout(int64_t T, int64_t V, int64_t H);
